@@ -1,6 +1,7 @@
 // csa2.cu -- C-ABI entry points of the CSA2 FP4 sparse-decode library:
 // argument validation, workspace layout and kernel launches. The kernels are
-// in quant.cuh (K1), indexer.cuh (K2), topk.cuh (K3) and attn.cuh (K4/K5).
+// in quant.cuh (K1), indexer.cuh (K2), topk.cuh (K3), attn.cuh (K4/K5),
+// pool.cuh (K6), replay.cuh (K9), rope.cuh (K10/K11) and gattn.cuh (K12/K13).
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -14,6 +15,8 @@
 #include "topk.cuh"
 #include "pool.cuh"
 #include "replay.cuh"
+#include "rope.cuh"
+#include "gattn.cuh"
 
 namespace csa2 {
 
@@ -73,6 +76,9 @@ cudaError_t device_info(DeviceInfo **out) {
         e = cudaFuncSetAttribute(swa_replay_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(kRpSmemBytes));
         if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(group_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(sizeof(GaSmem)));
+        if (e != cudaSuccess) return e;
         // One shared-memory carveout for every kernel of the path, so that
         // consecutive launches do not reconfigure the SMs' L1 / shared split.
         const void *kernels[] = {reinterpret_cast<const void *>(quant_kv_fp4_kernel),
@@ -85,7 +91,10 @@ cudaError_t device_info(DeviceInfo **out) {
                                  reinterpret_cast<const void *>(quant_index_fp8_kernel),
                                  reinterpret_cast<const void *>(pool_topk_kernel),
                                  reinterpret_cast<const void *>(lse_merge_kernel),
-                                 reinterpret_cast<const void *>(swa_replay_kernel)};
+                                 reinterpret_cast<const void *>(swa_replay_kernel),
+                                 reinterpret_cast<const void *>(append_kv_rope_kernel),
+                                 reinterpret_cast<const void *>(rope_rows_kernel),
+                                 reinterpret_cast<const void *>(group_attn_kernel)};
         for (const void *kf : kernels) {
             e = cudaFuncSetAttribute(kf, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
             if (e != cudaSuccess) return e;
@@ -191,6 +200,23 @@ csa2_status cuda_status(cudaError_t e) { return e == cudaSuccess ? CSA2_OK : CSA
 
 bool cache_ok(const csa2_paged_cache *c) {
     return c != nullptr && c->num_pages > 0 && c->num_pages <= (INT64_C(1) << 31) / kPage;
+}
+
+// A rotation of rows of `channels` channels; pairs of channels stay whole.
+bool rope_ok(const csa2_rope *r, int channels) {
+    return r->inv_freq != nullptr && r->dim >= 2 && r->dim % 2 == 0 && r->offset >= 0 && r->offset % 2 == 0 &&
+           r->dim <= channels && r->offset <= channels - r->dim && (r->interleaved == 0 || r->interleaved == 1);
+}
+
+RopeArgs rope_args(const csa2_rope *r) {
+    RopeArgs a = {};
+    if (r != nullptr) {
+        a.inv_freq = r->inv_freq;
+        a.half = r->dim / 2;
+        a.offset = r->offset;
+        a.interleaved = r->interleaved;
+    }
+    return a;
 }
 
 }  // namespace
@@ -551,6 +577,120 @@ csa2_status csa2_sparse_attn_decode_noalloc(const void *q_bf16, int B, int Sq, i
     return csa2_sparse_attn_decode(q_bf16, B, Sq, H, D, cache, page_table, max_pages, seq_lens, topk_idx, k,
                                    swa_bf16, W, softmax_scale, out, lse, g_noalloc_ptr[dev],
                                    CSA2_NOALLOC_SCRATCH_BYTES, stream);
+}
+
+csa2_status csa2_append_kv_rope(const void *x_bf16, int64_t x_stride, int64_t n_tok, int dim, const int32_t *positions,
+                                const int32_t *slot_mapping, const csa2_rope *rope, const void *kidx_bf16,
+                                int64_t kidx_stride, const csa2_rope *kidx_rope, const csa2_paged_cache *cache,
+                                void *stream) {
+    if (n_tok < 0 || !cache_ok(cache) || !rope) return CSA2_ERR_INVALID_ARG;
+    if (dim != kDim) return CSA2_ERR_UNSUPPORTED;
+    if (!rope_ok(rope, kDim) || (kidx_rope && (!kidx_bf16 || !rope_ok(kidx_rope, kIdxDim))))
+        return CSA2_ERR_INVALID_ARG;
+    if (x_stride < kDim || (kidx_bf16 && kidx_stride < kIdxDim)) return CSA2_ERR_INVALID_ARG;
+    if (n_tok == 0) return CSA2_OK;
+    if (!x_bf16 || !positions || !slot_mapping || !cache->kv_fp4 || !cache->kv_scale) return CSA2_ERR_INVALID_ARG;
+    if (kidx_bf16 && (!cache->kidx || !cache->kidx_scale)) return CSA2_ERR_INVALID_ARG;
+    if (!aligned(x_bf16, 16) || x_stride % 8 != 0 || !aligned(cache->kv_fp4, 16) || !aligned(positions, 4) ||
+        !aligned(slot_mapping, 4) || !aligned(rope->inv_freq, 4) || (kidx_rope && !aligned(kidx_rope->inv_freq, 4)) ||
+        (kidx_bf16 && (!aligned(kidx_bf16, 16) || kidx_stride % 8 != 0 || !aligned(cache->kidx, 16) ||
+                       !aligned(cache->kidx_scale, 16))))
+        return CSA2_ERR_ALIGNMENT;
+    if (n_tok > (INT64_C(1) << 31) || x_stride > (INT64_C(1) << 31) || kidx_stride > (INT64_C(1) << 31))
+        return CSA2_ERR_UNSUPPORTED;
+    DeviceInfo *dev = nullptr;
+    if (device_info(&dev) != cudaSuccess) return CSA2_ERR_CUDA;
+    AppendArgs A = {};
+    A.x = static_cast<const uint16_t *>(x_bf16);
+    A.x_stride = x_stride;
+    A.n = n_tok;
+    A.pos = positions;
+    A.slots = slot_mapping;
+    A.rope = rope_args(rope);
+    A.k = static_cast<const uint16_t *>(kidx_bf16);
+    A.k_stride = kidx_stride;
+    A.krope = rope_args(kidx_rope);
+    A.shared_angles = kidx_rope && kidx_rope->inv_freq == rope->inv_freq && kidx_rope->dim <= rope->dim;
+    A.kv_fp4 = static_cast<uint8_t *>(cache->kv_fp4);
+    A.kv_scale = static_cast<uint8_t *>(cache->kv_scale);
+    A.kidx = static_cast<uint8_t *>(cache->kidx);
+    A.kidx_scale = cache->kidx_scale;
+    A.n_slots = cache->num_pages * kPage;
+    return cuda_status(launch_append_kv_rope(A, static_cast<cudaStream_t>(stream)));
+}
+
+csa2_status csa2_rope_rows(const void *x_bf16, int64_t x_stride, int64_t n_tok, int heads, int dim,
+                           const int32_t *positions, const csa2_rope *rope, void *out_bf16, int64_t out_stride,
+                           void *stream) {
+    if (n_tok < 0 || heads <= 0 || dim <= 0 || !rope) return CSA2_ERR_INVALID_ARG;
+    if (dim > kDim || dim % 8 != 0 || heads > 1024 || n_tok > (INT64_C(1) << 31)) return CSA2_ERR_UNSUPPORTED;
+    if (!rope_ok(rope, dim)) return CSA2_ERR_INVALID_ARG;
+    const int64_t row = static_cast<int64_t>(heads) * dim;
+    if (x_stride < row || out_stride < row || x_stride > (INT64_C(1) << 31) || out_stride > (INT64_C(1) << 31))
+        return CSA2_ERR_INVALID_ARG;
+    if (n_tok == 0) return CSA2_OK;
+    if (!x_bf16 || !positions || !out_bf16 || (x_bf16 == out_bf16 && x_stride != out_stride))
+        return CSA2_ERR_INVALID_ARG;
+    if (!aligned(x_bf16, 16) || !aligned(out_bf16, 16) || x_stride % 8 != 0 || out_stride % 8 != 0 ||
+        !aligned(positions, 4) || !aligned(rope->inv_freq, 4))
+        return CSA2_ERR_ALIGNMENT;
+    DeviceInfo *dev = nullptr;
+    if (device_info(&dev) != cudaSuccess) return CSA2_ERR_CUDA;
+    RopeRowsArgs A = {};
+    A.x = static_cast<const uint16_t *>(x_bf16);
+    A.out = static_cast<uint16_t *>(out_bf16);
+    A.x_stride = x_stride;
+    A.out_stride = out_stride;
+    A.n = n_tok;
+    A.heads = heads;
+    A.dim = dim;
+    A.pos = positions;
+    A.rope = rope_args(rope);
+    return cuda_status(launch_rope_rows(A, static_cast<cudaStream_t>(stream)));
+}
+
+size_t csa2_group_attn_workspace_bytes(int N, int G) {
+    if (N <= 0 || G <= 0 || N > kGaMaxTokens || G > kGaMaxGroups) return 0;
+    return 256;
+}
+
+csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D, const csa2_paged_cache *cache,
+                            const int32_t *page_table, int G, int max_pages, const int32_t *kv_lens,
+                            const int32_t *q_offsets, float softmax_scale, const float *o_own, const float *lse_own,
+                            void *out_bf16, float *lse, void *ws, size_t ws_bytes, void *stream) {
+    if (H != kHeads || D != kDim) return CSA2_ERR_UNSUPPORTED;
+    if (N <= 0 || G <= 0 || max_pages <= 0 || !cache_ok(cache) || !std::isfinite(softmax_scale) ||
+        (o_own == nullptr) != (lse_own == nullptr))
+        return CSA2_ERR_INVALID_ARG;
+    if (N > kGaMaxTokens || G > kGaMaxGroups || static_cast<int64_t>(max_pages) * kPage > (INT64_C(1) << 30))
+        return CSA2_ERR_UNSUPPORTED;
+    if (!q_bf16 || !page_table || !kv_lens || !q_offsets || !out_bf16 || !lse || !cache->kv_fp4 || !cache->kv_scale)
+        return CSA2_ERR_INVALID_ARG;
+    if (!aligned(q_bf16, 16) || !aligned(cache->kv_fp4, 16) || !aligned(cache->kv_scale, 16) || !aligned(out_bf16, 16) ||
+        !aligned(lse, 4) || !aligned(page_table, 4) || !aligned(kv_lens, 4) || !aligned(q_offsets, 4) ||
+        !aligned(o_own, 16) || !aligned(lse_own, 4))
+        return CSA2_ERR_ALIGNMENT;
+    DeviceInfo *dev = nullptr;
+    if (device_info(&dev) != cudaSuccess) return CSA2_ERR_CUDA;
+    if (!ws || !aligned(ws, 256) || ws_bytes < csa2_group_attn_workspace_bytes(N, G)) return CSA2_ERR_WORKSPACE;
+    GaArgs A = {};
+    A.q = static_cast<const __nv_bfloat16 *>(q_bf16);
+    A.kv_fp4 = static_cast<const uint8_t *>(cache->kv_fp4);
+    A.kv_scale = static_cast<const uint8_t *>(cache->kv_scale);
+    A.num_pages = cache->num_pages;
+    A.page_table = page_table;
+    A.max_pages = max_pages;
+    A.kv_lens = kv_lens;
+    A.q_offsets = q_offsets;
+    A.N = N;
+    A.G = G;
+    A.scale_log2 = softmax_scale * 1.4426950408889634f;
+    A.o_own = o_own;
+    A.lse_own = lse_own;
+    A.out = static_cast<__nv_bfloat16 *>(out_bf16);
+    A.lse = lse;
+    return cuda_status(launch_pdl(group_attn_kernel, dim3(N), dim3(kGaThreads), sizeof(GaSmem),
+                                  static_cast<cudaStream_t>(stream), A));
 }
 
 csa2_status csa2_plan(const int *modes, int n_layers, int *kv_owner, int *index_src) {

@@ -161,6 +161,69 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
     return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
 }
 
+// One row's quantisation, shared by four neighbouring lanes (gmask): this
+// lane's 16 channels as bf16 pairs w (channels 8t .. 8t + 7, then
+// 32 + 8t .. 32 + 8t + 7) become the packed codes o; every lane gets sigma.
+__device__ __forceinline__ void fp8_row_codes(const uint32_t (&w)[8], unsigned gmask, float &sg, uint32_t (&o)[4]) {
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
+    amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, 2));
+    // sigma = RN(amax / 448): one rounded product and one fma
+    // correction (equal to the IEEE quotient for every finite bf16
+    // amax, checked exhaustively on the host).
+    const float q0 = __fmul_rn(amax, 1.0f / 448.0f);
+    sg = __fmaf_rn(__fmaf_rn(-q0, 448.0f, amax), 1.0f / 448.0f, q0);
+    // Scaled domain for tiny sigma (exact power-of-two scaling): a =
+    // |x| scl, s2 = sigma scl, p = a / s2 through inv = scl / s2;
+    // below 2^-120 the inputs themselves are scaled (inv would overflow).
+    const float scl = sg < 0x1p-100f ? 0x1p64f : 1.0f;
+    const float s2 = sg * scl;
+    float inv = rcp_approx(s2) * scl, ascl = scl;
+    if (sg < 0x1p-120f) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] *= scl;
+        inv = rcp_approx(s2);
+        ascl = 1.0f;
+    }
+    uint32_t mag[8];                                    // code pairs (2i, 2i + 1)
+    uint32_t near = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float p0 = fabsf(f[2 * i]) * inv, p1 = fabsf(f[2 * i + 1]) * inv;
+        const uint32_t lo = e4m3x2(p0 * 0.99999952316284180f, p1 * 0.99999952316284180f);   // 1 - 2^-21
+        const uint32_t hi = e4m3x2(p0 * 1.00000047683715820f, p1 * 1.00000047683715820f);   // 1 + 2^-21
+        mag[i] = lo;
+        near |= lo != hi ? (1u << i) : 0u;
+    }
+    if (__any_sync(gmask, near != 0u)) {                // rare: exact fix-up of close calls
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (near & (1u << i)) {
+                const float a0 = fabsf(f[2 * i]) * ascl, a1 = fabsf(f[2 * i + 1]) * ascl;
+                const float p0 = fabsf(f[2 * i]) * inv, p1 = fabsf(f[2 * i + 1]) * inv;
+                mag[i] = e4m3_quotient_fixup(a0, s2, p0) | (e4m3_quotient_fixup(a1, s2, p1) << 8);
+            }
+        }
+    }
+    o[0] = o[1] = o[2] = o[3] = 0u;
+    if (sg != 0.0f) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t m4 = __byte_perm(mag[2 * j], mag[2 * j + 1], 0x5410);     // 4 magnitudes
+            const uint32_t sgn = __byte_perm(w[2 * j], w[2 * j + 1], 0x7531) & 0x80808080u;
+            o[j] = m4 | (sgn & __vcmpne4(m4, 0u));                                  // canonical +0
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kIdxQuantThreads, 3)
 quant_index_fp8_kernel(const uint4 *__restrict__ x, int64_t n_rows, uint2 *__restrict__ codes,
                        float *__restrict__ sigma) {
@@ -196,63 +259,9 @@ quant_index_fp8_kernel(const uint4 *__restrict__ x, int64_t n_rows, uint2 *__res
             const uint4 va = stage[k % kIdxQuantStages][threadIdx.x][0];
             const uint4 vb = stage[k % kIdxQuantStages][threadIdx.x][1];
             const uint32_t w[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-            float f[16];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f[2 * i] = __uint_as_float(w[i] << 16);
-                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-            float amax = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
-            amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, 2));
-            // sigma = RN(amax / 448): one rounded product and one fma
-            // correction (equal to the IEEE quotient for every finite bf16
-            // amax, checked exhaustively on the host).
-            const float q0 = __fmul_rn(amax, 1.0f / 448.0f);
-            const float sg = __fmaf_rn(__fmaf_rn(-q0, 448.0f, amax), 1.0f / 448.0f, q0);
-            // Scaled domain for tiny sigma (exact power-of-two scaling): a =
-            // |x| scl, s2 = sigma scl, p = a / s2 through inv = scl / s2;
-            // below 2^-120 the inputs themselves are scaled (inv would overflow).
-            const float scl = sg < 0x1p-100f ? 0x1p64f : 1.0f;
-            const float s2 = sg * scl;
-            float inv = rcp_approx(s2) * scl, ascl = scl;
-            if (sg < 0x1p-120f) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] *= scl;
-                inv = rcp_approx(s2);
-                ascl = 1.0f;
-            }
-            uint32_t mag[8];                                    // code pairs (2i, 2i + 1)
-            uint32_t near = 0u;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float p0 = fabsf(f[2 * i]) * inv, p1 = fabsf(f[2 * i + 1]) * inv;
-                const uint32_t lo = e4m3x2(p0 * 0.99999952316284180f, p1 * 0.99999952316284180f);   // 1 - 2^-21
-                const uint32_t hi = e4m3x2(p0 * 1.00000047683715820f, p1 * 1.00000047683715820f);   // 1 + 2^-21
-                mag[i] = lo;
-                near |= lo != hi ? (1u << i) : 0u;
-            }
-            if (__any_sync(0xffffffffu, near != 0u)) {          // rare: exact fix-up of close calls
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (near & (1u << i)) {
-                        const float a0 = fabsf(f[2 * i]) * ascl, a1 = fabsf(f[2 * i + 1]) * ascl;
-                        const float p0 = fabsf(f[2 * i]) * inv, p1 = fabsf(f[2 * i + 1]) * inv;
-                        mag[i] = e4m3_quotient_fixup(a0, s2, p0) | (e4m3_quotient_fixup(a1, s2, p1) << 8);
-                    }
-                }
-            }
-            uint32_t o[4] = {0u, 0u, 0u, 0u};
-            if (sg != 0.0f) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t m4 = __byte_perm(mag[2 * j], mag[2 * j + 1], 0x5410);     // 4 magnitudes
-                    const uint32_t sgn = __byte_perm(w[2 * j], w[2 * j + 1], 0x7531) & 0x80808080u;
-                    o[j] = m4 | (sgn & __vcmpne4(m4, 0u));                                  // canonical +0
-                }
-            }
+            float sg;
+            uint32_t o[4];
+            fp8_row_codes(w, gmask, sg, o);
             if (row < n_rows) {
                 codes[row * 8 + part] = make_uint2(o[0], o[1]);           // channels 8t .. 8t + 7
                 codes[row * 8 + 4 + part] = make_uint2(o[2], o[3]);       // channels 32 + 8t ..

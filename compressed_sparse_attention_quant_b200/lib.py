@@ -27,7 +27,8 @@ STATUS = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED", 3:
 EXPORTS = ("csa2_quant_kv_fp4", "csa2_quant_indexer_fp8", "csa2_indexer_topk_workspace_bytes",
            "csa2_indexer_topk", "csa2_indexer_pool_topk", "csa2_sparse_attn_workspace_bytes", "csa2_sparse_attn_decode",
            "csa2_sparse_attn_decode_noalloc", "csa2_indexer_topk_scores", "csa2_topk_merge", "csa2_lse_merge",
-           "csa2_swa_replay_attn",
+           "csa2_swa_replay_attn", "csa2_append_kv_rope", "csa2_rope_rows", "csa2_group_attn_workspace_bytes",
+           "csa2_group_attn",
            "csa2_plan",
            "csa2_last_device_error", "csa2_status_string", "csa2_launch_count")
 
@@ -43,9 +44,15 @@ class _Cache(ctypes.Structure):
                 ("kidx_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("dim", ctypes.c_int), ("offset", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _cp = ctypes.POINTER(_Cache)
 _ip = ctypes.POINTER(ctypes.c_int)
+_rp = ctypes.POINTER(_Rope)
 
 
 def _load():
@@ -71,6 +78,11 @@ def _load():
         "csa2_topk_merge": (_i32, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
         "csa2_lse_merge": (_i32, [_vp, _vp, _i32, _i32, _vp, _vp, _vp]),
         "csa2_swa_replay_attn": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _f32, _vp, _vp, _vp]),
+        "csa2_append_kv_rope": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _rp, _vp, _i64, _rp, _cp, _vp]),
+        "csa2_rope_rows": (_i32, [_vp, _i64, _i64, _i32, _i32, _vp, _rp, _vp, _i64, _vp]),
+        "csa2_group_attn_workspace_bytes": (_sz, [_i32, _i32]),
+        "csa2_group_attn": (_i32, [_vp, _i32, _i32, _i32, _cp, _vp, _i32, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _vp,
+                                   _vp, _sz, _vp]),
         "csa2_plan": (_i32, [_ip, _i32, _ip, _ip]),
         "csa2_last_device_error": (_i32, [_vp]),
         "csa2_status_string": (ctypes.c_char_p, [_i32]),
@@ -381,6 +393,124 @@ def sparse_attn_decode_noalloc(q: torch.Tensor, cache: PagedCache, page_table: t
                                             _ptr(swa), WINDOW, float(softmax_scale), _ptr(out), _ptr(lse),
                                             _stream())
     _check("csa2_sparse_attn_decode_noalloc", rc)
+
+
+class Rope:
+    """A position rotation: the 2 * len(inv_freq) channels from `offset` on turn in pairs, (2i, 2i + 1) when
+    `interleaved`, else (i, i + len(inv_freq)); see csa2_rope in csa2.h."""
+
+    def __init__(self, inv_freq: torch.Tensor, offset: int = 0, interleaved: bool = False):
+        _req(inv_freq, torch.float32, "inv_freq")
+        if inv_freq.dim() != 1 or inv_freq.numel() == 0:
+            raise ValueError(f"inv_freq: expected one frequency per pair, got shape {tuple(inv_freq.shape)}")
+        self.inv_freq = inv_freq                       # kept alive: the descriptor holds its address
+        self.dim, self.offset, self.interleaved = 2 * inv_freq.numel(), int(offset), bool(interleaved)
+        self.desc = _Rope(inv_freq.data_ptr(), self.dim, self.offset, int(self.interleaved))
+
+
+def _req_here(**tensors: Optional[torch.Tensor]) -> None:
+    """Kernels run on the current device: its tensors only."""
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != here:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{here}")
+
+
+def _req_rows(t: torch.Tensor, dtype, name: str, shape) -> int:
+    """A tensor whose rows (all dimensions but the first) are contiguous; returns the elements from row to row."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    row = 1
+    for d in shape[1:]:
+        row *= int(d)
+    if t.shape[0] <= 1:
+        if t.shape[0] == 1 and not t[0].is_contiguous():
+            raise ValueError(f"{name}: rows must be contiguous")
+        return row
+    if not t[0].is_contiguous() or t.stride(0) < row:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return int(t.stride(0))
+
+
+def append_kv_rope(x: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor, cache: PagedCache, rope: Rope,
+                   kidx: Optional[torch.Tensor] = None, kidx_rope: Optional[Rope] = None) -> None:
+    """Rotates the bf16 latents x [n, 576] (and indexer keys kidx [n, 64]) by their positions, quantises them and
+    writes them to their slots of the cache. Rows may be strided (a slice of a wider projection)."""
+    n = x.shape[0]
+    xs = _req_rows(x, torch.bfloat16, "x", (n, DIM))
+    ks = IDX_DIM if kidx is None else _req_rows(kidx, torch.bfloat16, "kidx", (n, IDX_DIM))
+    _req(positions, torch.int32, "positions", (n,))
+    _req(slots, torch.int32, "slot_mapping", (n,))
+    _req_here(x=x, positions=positions, slot_mapping=slots, cache=cache.kv_fp4, inv_freq=rope.inv_freq, kidx=kidx,
+              kidx_inv_freq=None if kidx_rope is None else kidx_rope.inv_freq)
+    rc = _L.csa2_append_kv_rope(_ptr(x), xs, n, DIM, _ptr(positions), _ptr(slots), ctypes.byref(rope.desc), _ptr(kidx),
+                                ks, None if kidx_rope is None else ctypes.byref(kidx_rope.desc),
+                                ctypes.byref(cache.desc), _stream())
+    _check("csa2_append_kv_rope", rc)
+
+
+def rope_rows(x: torch.Tensor, positions: torch.Tensor, rope: Rope, out: Optional[torch.Tensor] = None
+              ) -> torch.Tensor:
+    """Query rows x [n, heads, dim] bf16 rotated by their token's position; out may be x (in place)."""
+    if x.dim() != 3:
+        raise ValueError(f"x: expected [n, heads, dim], got shape {tuple(x.shape)}")
+    n, heads, dim = x.shape
+    xs = _req_rows(x, torch.bfloat16, "x", (n, heads, dim))
+    _req(positions, torch.int32, "positions", (n,))
+    if out is None:
+        out = torch.empty(n, heads, dim, dtype=torch.bfloat16, device=x.device)
+    os_ = _req_rows(out, torch.bfloat16, "out", (n, heads, dim))
+    _req_here(x=x, positions=positions, inv_freq=rope.inv_freq, out=out)
+    rc = _L.csa2_rope_rows(_ptr(x), xs, n, heads, dim, _ptr(positions), ctypes.byref(rope.desc), _ptr(out), os_,
+                           _stream())
+    _check("csa2_rope_rows", rc)
+    return out
+
+
+def group_attn_workspace_bytes(N: int, G: int) -> int:
+    return int(_L.csa2_group_attn_workspace_bytes(N, G))
+
+
+def group_attn(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
+               q_offsets: torch.Tensor, softmax_scale: float, o_own: Optional[torch.Tensor] = None,
+               lse_own: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None
+               ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of each group's query tokens over the entries the group shares, joined with the tokens' own parts:
+    q [N, 16, 576] bf16, page_table [G, max_pages], kv_lens [G], q_offsets [G + 1] -> (out [N, 16, 576] bf16,
+    lse [N, 16]). Tokens of no group keep what out and lse held."""
+    N = q.shape[0]
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: expected [G, max_pages], got shape {tuple(page_table.shape)}")
+    G, max_pages = page_table.shape
+    _req(q, torch.bfloat16, "q", (N, HEADS, DIM))
+    _req(page_table, torch.int32, "page_table")
+    _req(kv_lens, torch.int32, "kv_lens", (G,))
+    _req(q_offsets, torch.int32, "q_offsets", (G + 1,))
+    if (o_own is None) != (lse_own is None):
+        raise ValueError("o_own and lse_own: give both or neither")
+    if o_own is not None:
+        _req(o_own, torch.float32, "o_own", (N, HEADS, DIM))
+        _req(lse_own, torch.float32, "lse_own", (N, HEADS))
+    if out is None:
+        out = torch.empty(N, HEADS, DIM, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty(N, HEADS, dtype=torch.float32, device=q.device)
+    _req(out, torch.bfloat16, "out", (N, HEADS, DIM))
+    _req(lse, torch.float32, "lse", (N, HEADS))
+    if ws is None:
+        ws = workspace(group_attn_workspace_bytes(N, G), q.device)
+    _req_here(q=q, cache=cache.kv_fp4, page_table=page_table, kv_lens=kv_lens, q_offsets=q_offsets, o_own=o_own,
+              lse_own=lse_own, out=out, lse=lse, ws=ws)
+    rc = _L.csa2_group_attn(_ptr(q), N, HEADS, DIM, ctypes.byref(cache.desc), _ptr(page_table), G, max_pages,
+                            _ptr(kv_lens), _ptr(q_offsets), float(softmax_scale), _ptr(o_own), _ptr(lse_own),
+                            _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream())
+    _check("csa2_group_attn", rc)
+    return out, lse
 
 
 def plan(modes: Sequence[str]) -> Tuple[list, list]:

@@ -401,6 +401,112 @@ csa2_status csa2_swa_replay_attn(const void *q_bf16, int B, int L, int H, int D,
                                  float softmax_scale, float *out, float *lse, void *stream);
 
 /*
+ * csa2_rope -- a position rotation of rows: `dim` channels starting at channel
+ * `offset` (both even) turn in dim / 2 pairs, the rest stay. Pair i turns by
+ * theta = position * inv_freq[i]:
+ *     a' = a cos(theta) - b sin(theta),   b' = a sin(theta) + b cos(theta)
+ * and holds channels (2i, 2i + 1) of the rotated ones when `interleaved` is 1,
+ * (i, i + dim / 2) when it is 0. Angles and products are binary64; the result
+ * is rounded to binary32 and then to bf16. A host-side struct; inv_freq is
+ * device float [dim / 2], finite.
+ */
+typedef struct csa2_rope {
+    const float *inv_freq;
+    int dim;
+    int offset;
+    int interleaved;
+} csa2_rope;
+
+/*
+ * csa2_append_kv_rope -- csa2_quant_kv_fp4 for rows that still lack their
+ * position: rotates each token's latent, quantises it and writes it to its
+ * slot, and (when kidx_bf16 is not NULL) rotates, quantises and writes its
+ * indexer key, all in one launch. The bytes are those of rotating both rows
+ * with csa2_rope_rows, quantising the key with csa2_quant_indexer_fp8 and
+ * appending with csa2_quant_kv_fp4. Inputs must be finite.
+ *
+ *   x_bf16        device bf16 [n_tok] rows of 576 channels, x_stride elements
+ *                 from row to row (>= 576, a multiple of 8), 16-byte aligned
+ *   positions     device int32 [n_tok]; a position of a kept token outside
+ *                 [0, 2^29) sets CSA2_ERR_DEVICE_BOUNDS and skips the token
+ *   slot_mapping  device int32 [n_tok], as csa2_quant_kv_fp4: a negative slot
+ *                 skips the token (its position is not looked at), a slot
+ *                 >= 64 * num_pages sets CSA2_ERR_DEVICE_BOUNDS. Slots of one
+ *                 call must differ: with two tokens for one slot, each 16-channel
+ *                 group of it holds one of the two.
+ *   rope          host pointer: rotation of the latent
+ *   kidx_bf16     device bf16 [n_tok] rows of 64 channels, kidx_stride elements
+ *                 apart (>= 64, a multiple of 8), 16-byte aligned; or NULL
+ *   kidx_rope     host pointer: rotation of the indexer key, NULL for none.
+ *                 Where it has the latent's inv_freq and no more pairs, one
+ *                 sine and cosine serve both.
+ * Per token 1,152 (+ 128) B are read and 324 (+ 68) B written.
+ */
+csa2_status csa2_append_kv_rope(const void *x_bf16, int64_t x_stride, int64_t n_tok, int dim,
+                                const int32_t *positions, const int32_t *slot_mapping,
+                                const csa2_rope *rope, const void *kidx_bf16,
+                                int64_t kidx_stride, const csa2_rope *kidx_rope,
+                                const csa2_paged_cache *cache, void *stream);
+
+/*
+ * csa2_rope_rows -- rotates query rows (attention or indexer queries) by their
+ * token's position, in place or into another tensor.
+ *
+ *   x_bf16, out_bf16  device bf16 [n_tok][heads][dim], x_stride / out_stride
+ *                     elements from token to token (>= heads * dim, a multiple
+ *                     of 8), 16-byte aligned. out_bf16 may be x_bf16 with the
+ *                     same stride; otherwise the two must not overlap.
+ *   positions         device int32 [n_tok]; one outside [0, 2^29) sets
+ *                     CSA2_ERR_DEVICE_BOUNDS and leaves its token's output as
+ *                     it was
+ * Limits: dim <= 576 and a multiple of 8, heads <= 1024.
+ */
+csa2_status csa2_rope_rows(const void *x_bf16, int64_t x_stride, int64_t n_tok, int heads, int dim,
+                           const int32_t *positions, const csa2_rope *rope, void *out_bf16,
+                           int64_t out_stride, void *stream);
+
+/*
+ * csa2_group_attn -- attention over entries that a group of query tokens
+ * shares. Group g owns query tokens q_offsets[g] .. q_offsets[g + 1) and all of
+ * them attend to the first kv_lens[g] entries of page_table[g] (keys = values,
+ * no causal bound), read and dequantised once for up to 8 tokens x 16 heads:
+ *     out[n][h] = sum_t softmax_t(scale * <q, key_t>) * key_t
+ *     lse[n][h] = log sum_t exp(scale * <q, key_t>)
+ * With o_own and lse_own (a normalised result and its natural-log lse over
+ * other keys, as csa2_sparse_attn_decode writes them; lse_own = -inf for no
+ * key) out and lse are those of the union, as by csa2_lse_merge.
+ *   - One group with a batch's tokens: a prefix that the batch shares, each
+ *     token's own part being its window and its selected later entries.
+ *   - One group per sequence: cross attention to the states of an encoder.
+ * A group without entries leaves its tokens their own part (out = 0 and
+ * lse = -inf without one).
+ *
+ *   q_bf16      device bf16 [N][16][576]
+ *   page_table  device int32 [G][max_pages]; a bad entry sets
+ *               CSA2_ERR_DEVICE_BOUNDS and its 64 entries are left out
+ *   kv_lens     device int32 [G]; one outside [0, 64 * max_pages] sets
+ *               CSA2_ERR_DEVICE_BOUNDS and counts as 0
+ *   q_offsets   device int32 [G + 1], ascending in [0, N]; a group whose two
+ *               bounds are not sets CSA2_ERR_DEVICE_BOUNDS and is left out.
+ *               Tokens of no group keep what out and lse held.
+ *   o_own       device float [N][16][576], or NULL; lse_own float [N][16]
+ *   out         device bf16 [N][16][576];  lse device float [N][16]. Neither
+ *               may overlap another argument.
+ *   ws          device workspace of csa2_group_attn_workspace_bytes(N, G)
+ *               bytes, 256-byte aligned, clobbered; calls that can overlap in
+ *               time need workspaces of their own
+ * Queries are carried in f16 under a power-of-two exponent per (token, head),
+ * probabilities are rounded to f16 (the output has bf16's 8 bits), scores,
+ * maxima, sums and outputs are fp32. Limits: N <= 2^20, G <= 65535.
+ */
+size_t csa2_group_attn_workspace_bytes(int N, int G);
+csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D,
+                            const csa2_paged_cache *cache, const int32_t *page_table, int G,
+                            int max_pages, const int32_t *kv_lens, const int32_t *q_offsets,
+                            float softmax_scale, const float *o_own, const float *lse_own,
+                            void *out_bf16, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
  * csa2_plan -- ownership bookkeeping for a group of layers ([ZUL section 3]:
  * KV owner layer -> consumer layers; [NEO part 2]: KV, indexer keys and top-K
  * indices shared across layers). Host-only, no device work.
