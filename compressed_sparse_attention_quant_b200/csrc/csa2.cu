@@ -77,7 +77,7 @@ cudaError_t device_info(DeviceInfo **out) {
                                  static_cast<int>(kRpSmemBytes));
         if (e != cudaSuccess) return e;
         e = cudaFuncSetAttribute(group_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(sizeof(GaSmem)));
+                                 static_cast<int>(kGaSmemBytes));
         if (e != cudaSuccess) return e;
         // One shared-memory carveout for every kernel of the path, so that
         // consecutive launches do not reconfigure the SMs' L1 / shared split.
@@ -94,7 +94,8 @@ cudaError_t device_info(DeviceInfo **out) {
                                  reinterpret_cast<const void *>(swa_replay_kernel),
                                  reinterpret_cast<const void *>(append_kv_rope_kernel),
                                  reinterpret_cast<const void *>(rope_rows_kernel),
-                                 reinterpret_cast<const void *>(group_attn_kernel)};
+                                 reinterpret_cast<const void *>(group_attn_kernel),
+                                 reinterpret_cast<const void *>(group_attn_merge_kernel)};
         for (const void *kf : kernels) {
             e = cudaFuncSetAttribute(kf, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
             if (e != cudaSuccess) return e;
@@ -651,7 +652,7 @@ csa2_status csa2_rope_rows(const void *x_bf16, int64_t x_stride, int64_t n_tok, 
 
 size_t csa2_group_attn_workspace_bytes(int N, int G) {
     if (N <= 0 || G <= 0 || N > kGaMaxTokens || G > kGaMaxGroups) return 0;
-    return 256;
+    return ga_ws_bytes(std::min(N, kGaTok));
 }
 
 csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D, const csa2_paged_cache *cache,
@@ -689,8 +690,16 @@ csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D, const csa2_
     A.lse_own = lse_own;
     A.out = static_cast<__nv_bfloat16 *>(out_bf16);
     A.lse = lse;
-    return cuda_status(launch_pdl(group_attn_kernel, dim3(N), dim3(kGaThreads), sizeof(GaSmem),
-                                  static_cast<cudaStream_t>(stream), A));
+    A.tok_slots = std::min(N, kGaTok);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    A.plan = reinterpret_cast<GaPlan *>(base);
+    A.part_ml = reinterpret_cast<float2 *>(base + ga_plan_bytes());
+    A.part_o = reinterpret_cast<float *>(base + ga_plan_bytes() + ga_ml_bytes(A.tok_slots));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int ctas = std::min(dev->sm_count, kGaMaxCtas);
+    cudaError_t e = launch_pdl(group_attn_kernel, dim3(ctas), dim3(kGaThreads), kGaSmemBytes, st, A);
+    if (e != cudaSuccess) return CSA2_ERR_CUDA;
+    return cuda_status(launch_pdl(group_attn_merge_kernel, dim3(4 * ctas), dim3(kGmThreads), 0, st, A));
 }
 
 csa2_status csa2_plan(const int *modes, int n_layers, int *kv_owner, int *index_src) {

@@ -1,10 +1,45 @@
-// gattn.cuh -- K12: group attention over the paged FP4 cache. Every query
+// gattn.cuh -- K12/K13: group attention over the paged FP4 cache. Every query
 // token of group g attends to the first kv_lens[g] entries of the group's
 // pages (keys = values), and the result is joined with the token's own part.
 //
-// One CTA per query token: blocks of 32 keys are dequantised to shared memory
-// once for the 16 heads, the scores go through a softmax with a running
-// maximum and sum per head, and each thread keeps 36 outputs in registers.
+// K12 runs both products on the tensor cores (tcgen05, accumulators in tensor
+// memory) for row tiles of 8 tokens x 16 heads = 128 rows and blocks of 64
+// keys (one page):
+//   S [128 x 64]   = Q [128 x 576] . K^T              (36 MMAs, K = 16)
+//   O [128 x 576] += P [128 x 64] . V, V = K          (4 MMAs per channel block)
+// Bound: the tensor pipe, 2,304 cycles a block at its nominal rate. What
+// decides the layout is that a row tile of 128 x 576 fp32 outputs (288 KB) is
+// more than tensor memory (256 KB), and that shared-memory traffic (Q and K
+// are read for S, V for O, and K is written once: 576 cycles each but Q's
+// 1,152) only stays below the MMA time with all 128 rows in one CTA. So the
+// first 416 channels of O accumulate in tensor memory; the other 160 come out
+// of the tensor cores block by block, 32 channels at a time, and are added up
+// in the registers of the softmax threads. Splitting the channels over two
+// CTAs would compute S twice (1.5 times the MMAs); 64 rows per CTA would read
+// and write K for half the rows.
+//
+// Shared memory holds Q (f16, 147,456 B) and one block of K (73,728 B) as
+// slabs of 8 channels (16 bytes) per row: the K-major operand layout of S and
+// the MN-major one of O, so the block is dequantised once for both. The
+// block's nine chunks of 64 channels are refilled one by one as O's MMAs
+// release them. Tensor memory: O columns 0-415, S 416-479, P (f16) 480-511;
+// the 32-channel pieces use the upper half of S, which is read by then.
+//   warps 0-7   load the query tile, then per block the softmax: thread = row,
+//               warps 0-3 the first 32 keys and 4-7 the others. Exp2 domain;
+//               the reference maximum rises only when a block exceeds it by
+//               more than 8 (O is rescaled then), otherwise probabilities up
+//               to 2^8 stay as they are, at the same relative precision.
+//               Probabilities are rounded to f16 for the MMA (2^-11, below the
+//               output's bf16); their sum is taken before, in fp32. Then they
+//               add the pieces, and at the end of a row tile write it.
+//   warps 8-11  dequantise: E2M1 x E4M3 is exact in f16.
+//   warp 12     one thread issues the MMAs (warps 13-15 only fill its warpgroup).
+// The work is one flat list of (row tile, block) steps, cut into equal
+// contiguous ranges, one per CTA; a row tile that lies in several ranges is
+// left as unnormalised partials (m, l, O) that K13 joins. Lengths and offsets
+// are read on the device, so a captured call serves other lengths.
+// Every wait is an mbarrier wait with a time limit; a thread whose wait ran
+// out goes on without waiting, so that all reach the end.
 #pragma once
 
 #include "attn.cuh"
@@ -13,9 +48,28 @@
 namespace csa2 {
 
 constexpr int kGaMaxTokens = 1 << 20, kGaMaxGroups = 65535;
-constexpr int kGaThreads = 256;
-constexpr int kGaKeys = 32;
-constexpr int kGaPer = kHeads * kDim / kGaThreads;                // 36 outputs per thread
+constexpr int kGaMaxCtas = 160;
+constexpr int kGaTok = 8;                                          // tokens per row tile
+constexpr int kGaRows = kGaTok * kHeads;                           // 128
+constexpr int kGaBlk = kPage;                                      // keys per block
+constexpr int kGaSoftWarps = 8, kGaDeqWarps = 4;
+constexpr int kGaMmaWarp = kGaSoftWarps + kGaDeqWarps;
+constexpr int kGaThreads = (kGaMmaWarp + 4) * 32;                  // 512: whole warpgroups, for the register split
+// Registers per thread: 128 at launch (512 x 128 = the SM's 65,536); the two
+// softmax warpgroups take 160, the other two 96: (160 + 160 + 96 + 96) x 128
+// threads = 65,536, the launch's own total.
+constexpr int kGaSoftRegs = 160, kGaOtherRegs = 96;
+constexpr int kGaChunk = 64;                                       // channels per chunk
+constexpr int kGaChunks = kDim / kGaChunk;                         // 9
+constexpr int kGaQSlab = kGaRows * 16, kGaKSlab = kGaBlk * 16;     // 2,048 and 1,024 B: 8 channels of every row
+constexpr int kGaTmemCh = 416;                                     // channels accumulated in tensor memory
+constexpr int kGaPiece = 32;
+constexpr int kGaPieces = (kDim - kGaTmemCh) / kGaPiece;           // 5
+constexpr int kGaSCol = kGaTmemCh, kGaPCol = kGaSCol + kGaBlk;     // 416, 480
+constexpr int kGaPieceCol = kGaSCol + kGaBlk - kGaPiece;           // 448
+constexpr int kGaRegs = kGaPieces * kGaPiece / 2;                  // outputs a softmax thread holds: 80
+constexpr float kGaSlack = 8.0f;                                   // log2 units a block may exceed the reference
+static_assert(kGaPCol + kGaBlk / 2 == 512, "tensor memory is full");
 
 struct GaArgs {
     const __nv_bfloat16 *q;            // [N][16][576]
@@ -26,111 +80,734 @@ struct GaArgs {
     const int32_t *kv_lens;            // [G]
     const int32_t *q_offsets;          // [G + 1]
     int N, G;
-    float scale_log2;
+    float scale_log2;                  // softmax scale * log2(e)
     const float *o_own, *lse_own;      // [N][16][576], [N][16], or null
     __nv_bfloat16 *out;                // [N][16][576]
     float *lse;                        // [N][16]
+    struct GaPlan *plan;
+    float *part_o;                     // [2 * CTAs][tok_slots][576][16]
+    float2 *part_ml;                   // [2 * CTAs][tok_slots * 16]: (m in the log2 domain, l)
+    int tok_slots;                     // min(8, N)
+};
+
+// What K13 has to know of K12's ranges.
+struct GaPlan {
+    int64_t total;                     // steps of all row tiles
+    int ctas;                          // ranges
+    struct Tile { int64_t begin; int blocks, tok0, ntok; } first[kGaMaxCtas];   // row tile of a range's first step
+};
+
+__host__ __device__ __forceinline__ int64_t ga_range(int64_t total, int c, int ctas) { return total * c / ctas; }
+
+struct GaGroup { int tok0, n, T, blocks; };
+
+// Group g as the kernel takes it: bounds outside [0, N] leave it without
+// tokens, a bad length without entries. A group without entries still has one
+// (empty) block per row tile, which writes its tokens' own parts.
+__device__ __forceinline__ GaGroup ga_group(const GaArgs &A, int g, bool report) {
+    GaGroup r;
+    r.tok0 = __ldg(A.q_offsets + g);
+    const int b = __ldg(A.q_offsets + g + 1);
+    r.T = __ldg(A.kv_lens + g);
+    bool bad = false;
+    r.n = b - r.tok0;
+    if (r.tok0 < 0 || b > A.N || b < r.tok0) {
+        bad = true;
+        r.n = 0;
+    }
+    if (r.T < 0 || r.T > A.max_pages * kPage) {
+        bad = true;
+        r.T = 0;
+    }
+    if (bad && report) flag_status(kStatusBounds);
+    r.blocks = max(1, (r.T + kPage - 1) / kPage);
+    return r;
+}
+
+__device__ __forceinline__ int64_t ga_steps(const GaGroup &g) {
+    return static_cast<int64_t>((g.n + kGaTok - 1) / kGaTok) * g.blocks;
+}
+
+// One row tile's blocks [k0, k1) of a CTA's range.
+struct GaSeg {
+    int g, tok0, ntok, T, blocks, k0, k1;
+};
+
+// Walks a range segment by segment; every role of the CTA does so by itself.
+struct GaWalk {
+    int64_t left;                      // steps to go
+    int g, tile, k;                    // group, row tile of the group, block of the row tile
+    __device__ __forceinline__ bool next(const GaArgs &A, GaSeg &s) {
+        if (left <= 0) return false;
+        GaGroup grp = ga_group(A, g, false);
+        while (tile * kGaTok >= grp.n) {
+            if (++g >= A.G) return false;
+            grp = ga_group(A, g, false);
+            tile = 0;
+        }
+        s.g = g;
+        s.tok0 = grp.tok0 + tile * kGaTok;
+        s.ntok = min(kGaTok, grp.n - tile * kGaTok);
+        s.T = grp.T;
+        s.blocks = grp.blocks;
+        s.k0 = k;
+        s.k1 = left < grp.blocks - k ? k + static_cast<int>(left) : grp.blocks;
+        left -= s.k1 - s.k0;
+        k = 0;
+        ++tile;
+        return true;
+    }
 };
 
 struct GaSmem {
-    float q[kHeads][kDim + 1];
-    float k[kGaKeys][kDim + 1];
-    float s[kHeads][kGaKeys + 1];
-    float m[kHeads], l[kHeads], f[kHeads];
+    alignas(1024) uint8_t q[kGaRows * kDim * 2];
+    alignas(1024) uint8_t k[kGaBlk * kDim * 2];
+    uint64_t q_full, s_full, p_full, d_full, d_empty, o_full;
+    uint64_t k_full[kGaChunks], k_free[kGaChunks];
+    uint32_t tmem;
+    int valid[2];                      // keys of a block that count, by block parity
+    float scale[kGaRows];              // a row's softmax scale (log2) times its query exponent
+    float mx[2][2][kGaRows];           // a row's maximum in each half of a block, by block parity
+    float l[kGaRows];
+    int64_t scan[kGaThreads / 32], start, total;
+    int start_g;
+    GaWalk walk;
+};
+constexpr size_t kGaSmemBytes = sizeof(GaSmem);
+static_assert(kGaSmemBytes <= 232448, "one CTA per SM");
+
+// ---------------------------------------------------------------- PTX
+__device__ __forceinline__ void ga_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// A from tensor memory: lane = row, a 32-bit column holds two f16 of the K side.
+__device__ __forceinline__ void ga_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ void ga_tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float ga_ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ void ga_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void ga_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ void ga_pair_bar(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// A wait that a thread gives up for good after its first timeout.
+struct GaWait {
+    bool dead = false;
+    __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
+        if (!dead) dead = !mbar_wait_bounded(bar, parity);
+    }
 };
 
-__global__ void __launch_bounds__(kGaThreads)
-group_attn_kernel(const GaArgs A) {
-    extern __shared__ uint8_t ga_raw[];
-    GaSmem &sm = *reinterpret_cast<GaSmem *>(ga_raw);
-    pdl_wait();
-    pdl_trigger();
-    const int tid = threadIdx.x, tok = blockIdx.x;
-    int g = -1;
-    for (int i = 0; i < A.G; ++i) {
-        const int a = A.q_offsets[i], b = A.q_offsets[i + 1];
-        if (a < 0 || b > A.N || b < a) {
-            if (tid == 0) flag_status(kStatusBounds);
-            continue;
+// ---------------------------------------------------------------- roles
+// The first step of this CTA's range: its group, and the totals.
+__device__ __forceinline__ void ga_locate(const GaArgs &A, GaSmem &sm) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kWarps = kGaThreads / 32;
+    int64_t mine = 0, total = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        int64_t base = 0, begin = 0, want = -1;
+        int ctas = 0;
+        if (pass == 1) {
+            ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+            want = static_cast<int>(blockIdx.x) < ctas ? ga_range(total, blockIdx.x, ctas) : -1;
+            if (tid == 0) {
+                sm.total = total;
+                sm.start_g = -1;
+            }
         }
-        if (tok >= a && tok < b) g = i;
-    }
-    if (g < 0) return;
-    int T = A.kv_lens[g];
-    if (T < 0 || T > A.max_pages * kPage) {
-        if (tid == 0) flag_status(kStatusBounds);
-        T = 0;
-    }
-    for (int i = tid; i < kHeads * kDim; i += kGaThreads)
-        sm.q[i / kDim][i % kDim] = __bfloat162float(A.q[static_cast<int64_t>(tok) * kHeads * kDim + i]);
-    if (tid < kHeads) {
-        sm.m[tid] = -INFINITY;
-        sm.l[tid] = 0.0f;
-    }
-    float acc[kGaPer];
+        for (int g0 = 0; g0 < A.G; g0 += kGaThreads) {
+            if (pass == 0 || A.G > kGaThreads)            // one chunk of groups is scanned from registers
+                mine = g0 + tid < A.G ? ga_steps(ga_group(A, g0 + tid, pass == 0 && blockIdx.x == 0)) : 0;
+            int64_t incl = mine;
 #pragma unroll
-    for (int i = 0; i < kGaPer; ++i) acc[i] = 0.0f;
-    for (int t0 = 0; t0 < T; t0 += kGaKeys) {
-        const int page = A.page_table[static_cast<int64_t>(g) * A.max_pages + t0 / kPage];
-        const bool page_ok = page >= 0 && page < A.num_pages;
-        if (!page_ok && tid == 0) flag_status(kStatusBounds);
-        const int n = page_ok ? min(kGaKeys, T - t0) : 0;
-        __syncthreads();
-        for (int i = tid; i < kGaKeys * (kDim / 2); i += kGaThreads) {
-            const int r = i / (kDim / 2), c = i % (kDim / 2);
-            float2 v = make_float2(0.0f, 0.0f);
-            if (r < n) {
-                const int64_t slot = static_cast<int64_t>(page) * kPage + (t0 + r) % kPage;
-                const uint32_t h = hmul2_u32(e2m1x2_to_f16x2(A.kv_fp4[slot * kFp4Bytes + c]),
-                                             e4m3x2_to_f16x2(A.kv_scale[slot * kScaleBytes + c / 8] * 0x101u));
-                v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += o;
             }
-            sm.k[r][2 * c] = v.x;
-            sm.k[r][2 * c + 1] = v.y;
-        }
-        __syncthreads();
-        for (int i = tid; i < kHeads * kGaKeys; i += kGaThreads) {
-            const int h = i / kGaKeys, r = i % kGaKeys;
-            float d = 0.0f;
-            for (int c = 0; c < kDim; ++c) d = fmaf(sm.q[h][c], sm.k[r][c], d);
-            sm.s[h][r] = r < n ? d * A.scale_log2 : -INFINITY;
-        }
-        __syncthreads();
-        if (tid < kHeads) {
-            float m = sm.m[tid];
-            for (int r = 0; r < kGaKeys; ++r) m = fmaxf(m, sm.s[tid][r]);
-            const float ref = m == -INFINITY ? 0.0f : m;
-            const float f = exp2f(sm.m[tid] - ref);
-            float l = 0.0f;
-            for (int r = 0; r < kGaKeys; ++r) {
-                const float p = exp2f(sm.s[tid][r] - ref);
-                sm.s[tid][r] = p;
-                l += p;
+            if (lane == 31) sm.scan[warp] = incl;
+            __syncthreads();
+            int64_t all = 0, before = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) before += sm.scan[w];
+                all += sm.scan[w];
             }
-            sm.m[tid] = m;
-            sm.l[tid] = sm.l[tid] * f + l;
-            sm.f[tid] = f;
+            begin = base + before + incl - mine;
+            if (want >= begin && want < begin + mine) {
+                sm.start_g = g0 + tid;
+                sm.start = begin;
+            }
+            base += all;
+            __syncthreads();
         }
-        __syncthreads();
+        total = base;
+    }
+}
+
+// Query tile -> f16 under a power-of-two exponent per row, one token per warp.
+__device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaSeg &s, int warp, int lane) {
 #pragma unroll 1
-        for (int i = 0; i < kGaPer; ++i) {
-            const int e = i * kGaThreads + tid, h = e / kDim, c = e % kDim;
-            float a = 0.0f;
-            for (int r = 0; r < kGaKeys; ++r) a = fmaf(sm.s[h][r], sm.k[r][c], a);
-            acc[i] = acc[i] * sm.f[h] + a;
+    for (int half = 0; half < 2; ++half) {
+        const int h = half * 8 + (lane & 7), row = warp * kHeads + h, part = lane >> 3;
+        uint4 v[18];
+        float mx = 0.0f;
+        const bool some = warp < s.ntok;
+        const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (static_cast<int64_t>(s.tok0 + (some ? warp : 0)) * kHeads + h) * kDim);
+#pragma unroll
+        for (int u = 0; u < 18; ++u) v[u] = some ? __ldg(src + 4 * u + part) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int u = 0; u < 18; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = bf16x2_f32((&v[u].x)[e]);
+                mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const int eq = f16_exponent(mx);
+        const float down = exp2f(static_cast<float>(-eq));
+        if (part == 0) sm.scale[row] = A.scale_log2 * exp2f(static_cast<float>(eq));
+#pragma unroll
+        for (int u = 0; u < 18; ++u) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = bf16x2_f32((&v[u].x)[e]);
+                o[e] = f32x2_f16x2(f.x * down, f.y * down);
+            }
+            *reinterpret_cast<uint4 *>(sm.q + (4 * u + part) * kGaQSlab + row * 16) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+    }
+}
+
+__device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk walk, int warp, int lane) {
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;      // keys 32 half ..; tile row
+    const uint32_t tm = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int pair_bar = 1 + (warp & 3);                           // the two warps of the same rows
+    GaWait wait;
+    uint32_t blk = 0, piece = 0, seg_no = 0;
+    GaSeg s;
+    while (walk.next(A, s)) {
+        ga_load_q(A, sm, s, warp, lane);
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 5, 256;" ::: "memory");             // scales of all rows; the tile is whole
+        if (threadIdx.x == 0) mbar_arrive(&sm.q_full);
+        const float scale = sm.scale[row];
+        float m = -INFINITY, l = 0.0f;
+        float acc[kGaRegs];
+#pragma unroll
+        for (int i = 0; i < kGaRegs; ++i) acc[i] = 0.0f;
+        for (int kb = s.k0; kb < s.k1; ++kb, ++blk) {
+            const uint32_t par = blk & 1u;
+            wait(&sm.s_full, par);
+            wait(&sm.k_full[kGaChunks - 1], par);                  // orders the read of valid[] as well
+            tc_fence_after();
+            float x[32];
+            {
+                float a[16];
+                tmem_ld16(tm + kGaSCol + 32 * half, a);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = a[i];
+                tmem_ld16(tm + kGaSCol + 32 * half + 16, a);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[16 + i] = a[i];
+            }
+            const int n = sm.valid[par] - 32 * half;
+            float mx = -INFINITY;
+            if (n >= 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    x[i] *= scale;
+                    mx = fmaxf(mx, x[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    x[i] = i < n ? x[i] * scale : -INFINITY;
+                    mx = fmaxf(mx, x[i]);
+                }
+            }
+            sm.mx[par][half][row] = mx;
+            ga_pair_bar(pair_bar);
+            mx = fmaxf(mx, sm.mx[par][half ^ 1][row]);
+            const bool raise = mx > m + kGaSlack || (m == -INFINITY && mx > m);
+            if (__any_sync(0xffffffffu, raise)) {
+                const float f = raise ? ga_ex2(m - mx) : 1.0f;     // 0 for the first keys of a row
+                if (raise) m = mx;
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < kGaRegs; ++i) acc[i] *= f;
+                if (kb > s.k0) {
+#pragma unroll 1
+                    for (int c = 0; c < kGaTmemCh / 2; c += 16) {
+                        float a[16];
+                        uint32_t o[16];
+                        const uint32_t at = tm + half * (kGaTmemCh / 2) + c;
+                        tmem_ld16(at, a);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(a[i] * f);
+                        ga_tmem_st16(at, o);
+                    }
+                }
+            }
+            const float ref = m == -INFINITY ? 0.0f : m;
+            float sum = 0.0f;
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float a = ga_ex2(x[2 * i] - ref), b = ga_ex2(x[2 * i + 1] - ref);
+                sum += a + b;
+                p[i] = f32x2_f16x2(a, b);
+            }
+            l += sum;
+            ga_tmem_st16(tm + kGaPCol + 16 * half, p);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full);
+            // the 32-channel pieces of this block
+#pragma unroll
+            for (int j = 0; j < kGaPieces; ++j, ++piece) {
+                wait(&sm.d_full, piece & 1u);
+                tc_fence_after();
+                float a[16];
+                tmem_ld16(tm + kGaPieceCol + 16 * half, a);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.d_empty);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[j * 16 + i] += a[i];
+            }
+        }
+        // ---- end of the segment
+        wait(&sm.o_full, seg_no & 1u);
+        tc_fence_after();
+        const int tok = row >> 4, h = row & 15;
+        const bool live = tok < s.ntok;
+        if (half == 1) sm.l[row] = l;
+        ga_pair_bar(pair_bar);
+        if (half == 0) sm.l[row] = l += sm.l[row];
+        ga_pair_bar(pair_bar);
+        l = sm.l[row];
+        if (s.k0 > 0 || s.k1 < s.blocks) {
+            // part of a row tile: unnormalised
+            const int64_t slot = 2 * blockIdx.x + (seg_no > 0);
+            float *po = A.part_o + (slot * A.tok_slots + tok) * (kDim * kHeads) + h;
+            if (live && half == 0) A.part_ml[(slot * A.tok_slots + tok) * kHeads + h] = make_float2(m, l);
+#pragma unroll 1
+            for (int c = 0; c < kGaTmemCh / 2; c += 16) {
+                float a[16];
+                tmem_ld16(tm + half * (kGaTmemCh / 2) + c, a);
+                if (live)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) po[(half * (kGaTmemCh / 2) + c + i) * kHeads] = a[i];
+            }
+            if (live)
+#pragma unroll
+                for (int i = 0; i < kGaRegs; ++i)
+                    po[(kGaTmemCh + (i >> 4) * kGaPiece + half * 16 + (i & 15)) * kHeads] = acc[i];
+        } else {
+            // the whole row tile: join the token's own part and write it
+            const int64_t r = static_cast<int64_t>(s.tok0 + (live ? tok : 0)) * kHeads + h;
+            const float lo = A.lse_own ? __ldg(A.lse_own + r) * 1.4426950408889634f : -INFINITY;
+            const float top = fmaxf(m, lo), ref = top == -INFINITY ? 0.0f : top;
+            const float wk = ga_ex2(m - ref), wo = ga_ex2(lo - ref);
+            const float sum = l * wk + wo;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float fk = wk * inv, fo = wo * inv;
+            if (live && half == 0)
+                A.lse[r] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+            auto write = [&](int ch, const float *a) {             // 16 channels from ch on
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = a[i] * fk;
+                if (wo > 0.0f) {
+                    const float4 *own = reinterpret_cast<const float4 *>(A.o_own + r * kDim + ch);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 o = __ldg(own + i);
+                        v[4 * i] += fo * o.x;
+                        v[4 * i + 1] += fo * o.y;
+                        v[4 * i + 2] += fo * o.z;
+                        v[4 * i + 3] += fo * o.w;
+                    }
+                }
+                uint32_t b[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    b[i] = *reinterpret_cast<const uint32_t *>(&t);
+                }
+                uint4 *dst = reinterpret_cast<uint4 *>(A.out + r * kDim + ch);
+                dst[0] = make_uint4(b[0], b[1], b[2], b[3]);
+                dst[1] = make_uint4(b[4], b[5], b[6], b[7]);
+            };
+#pragma unroll 1
+            for (int c = 0; c < kGaTmemCh / 2; c += 16) {
+                float a[16];
+                tmem_ld16(tm + half * (kGaTmemCh / 2) + c, a);
+                if (live) write(half * (kGaTmemCh / 2) + c, a);
+            }
+            if (live)
+#pragma unroll
+                for (int j = 0; j < kGaPieces; ++j) write(kGaTmemCh + j * kGaPiece + half * 16, acc + 16 * j);
+        }
+        tc_fence_before();
+        ++seg_no;
+    }
+}
+
+__device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk walk, int warp, int lane) {
+    const int key = warp * 16 + (lane & 15), part = lane >> 4;     // this thread's key and half of each chunk
+    GaWait wait;
+    uint4 raw[kGaChunks];                                          // 32 channels of each chunk: codes
+    uint32_t sc[kGaChunks];                                        // and their two E4M3 scales
+    const uint4 *codes = nullptr;
+    const uint16_t *scales = nullptr;
+    bool ok = false;                                               // the key counts; one that does not is zeros
+    GaSeg s = {};
+    int kb = 0, n = 0;
+    auto open = [&]() {                                            // block kb of segment s
+        n = min(kGaBlk, s.T - kb * kGaBlk);
+        int page = 0;
+        if (n > 0) {
+            page = __ldg(A.page_table + static_cast<int64_t>(s.g) * A.max_pages + kb);
+            if (page < 0 || page >= A.num_pages) {
+                flag_status(kStatusBounds);
+                n = 0;
+            }
+        }
+        n = max(n, 0);
+        ok = key < n;
+        const int64_t slot = static_cast<int64_t>(page) * kPage + key;
+        codes = reinterpret_cast<const uint4 *>(A.kv_fp4 + slot * kFp4Bytes) + part;
+        scales = reinterpret_cast<const uint16_t *>(A.kv_scale + slot * kScaleBytes) + part;
+    };
+    auto load = [&](int c) {
+        raw[c] = ok ? __ldg(codes + 2 * c) : make_uint4(0u, 0u, 0u, 0u);
+        sc[c] = ok ? __ldg(scales + 2 * c) : 0u;
+    };
+    bool more = walk.next(A, s);
+    if (more) {
+        kb = s.k0;
+        open();
+#pragma unroll
+        for (int c = 0; c < kGaChunks; ++c) load(c);
+    }
+    for (uint32_t blk = 0; more; ++blk) {
+        if (warp == 0 && lane == 0) sm.valid[blk & 1u] = n;
+        if (++kb == s.k1) {                                        // the block after
+            more = walk.next(A, s);
+            kb = s.k0;
+        }
+        if (more) open();
+#pragma unroll
+        for (int c = 0; c < kGaChunks; ++c) {
+            if (blk > 0) wait(&sm.k_free[c], (blk - 1) & 1u);
+            const uint32_t s2 = e4m3x2_to_f16x2(sc[c]);
+            const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t w = (&raw[c].x)[u], f = u < 2 ? sa : sb;
+                *reinterpret_cast<uint4 *>(sm.k + (8 * c + 4 * part + u) * kGaKSlab + key * 16) =
+                    make_uint4(hmul2_u32(e2m1x2_to_f16x2(w & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2((w >> 8) & 0xffu), f),
+                               hmul2_u32(e2m1x2_to_f16x2((w >> 16) & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2(w >> 24), f));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.k_full[c]);
+            if (more) load(c);                                     // in flight until the next block's turn
+        }
+    }
+}
+
+__device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk) {
+    const uint32_t tm = sm.tmem;
+    // K-major: leading offset along K (8 channels), stride offset along the rows; MN-major: along the keys, along the channels
+    const uint64_t d_q = umma_desc(smem_u32(sm.q), kGaQSlab, 128, 0);
+    const uint64_t d_k = umma_desc(smem_u32(sm.k), kGaKSlab, 128, 0);
+    const uint64_t d_v = umma_desc(smem_u32(sm.k), 128, kGaKSlab, 0);
+    constexpr uint32_t id_qk = umma_idesc(kGaRows, kGaBlk, false, false);
+    GaWait wait;
+    uint32_t blk = 0, piece = 0, seg_no = 0;
+    GaSeg s;
+    while (walk.next(A, s)) {
+        wait(&sm.q_full, seg_no & 1u);
+        for (int kb = s.k0; kb < s.k1; ++kb, ++blk) {
+            const uint32_t par = blk & 1u, acc = kb > s.k0;
+            // S: the last piece of the block before has been read (it lies in S's columns)
+            if (piece > 0) wait(&sm.d_empty, (piece - 1) & 1u);
+            tc_fence_after();
+            for (int c = 0; c < kGaChunks; ++c) {
+                wait(&sm.k_full[c], par);
+#pragma unroll
+                for (int j = 0; j < kGaChunk / 16; ++j)
+                    ga_mma_ss(tm + kGaSCol, d_q + ((c * 8 + j * 2) * kGaQSlab >> 4), d_k + ((c * 8 + j * 2) * kGaKSlab >> 4),
+                              id_qk, (c | j) != 0);
+            }
+            umma_commit(&sm.s_full);
+            wait(&sm.p_full, par);
+            tc_fence_after();
+            // channels [ch, ch + N) of O or of a piece, K = 64 keys
+            auto pv = [&](auto n, int ch, uint32_t d, uint32_t a) {
+                constexpr uint32_t id = umma_idesc(kGaRows, decltype(n)::value, false, true);
+#pragma unroll
+                for (int j = 0; j < kGaBlk / 16; ++j)
+                    ga_mma_ts(tm + d, tm + kGaPCol + 8 * j, d_v + ((ch / 8 * kGaKSlab + j * 256) >> 4), id, a | (j > 0));
+            };
+            auto channels = [&](int c) {
+                pv(std::integral_constant<int, 64>{}, 64 * c, 64 * c, acc);
+                umma_commit(&sm.k_free[c]);
+            };
+            auto piece_mma = [&](int j) {
+                if (j > 0) {
+                    wait(&sm.d_empty, (piece - 1) & 1u);
+                    tc_fence_after();
+                }
+                pv(std::integral_constant<int, kGaPiece>{}, kGaTmemCh + kGaPiece * j, kGaPieceCol, 0u);
+                umma_commit(&sm.d_full);
+                ++piece;
+            };
+            piece_mma(0);
+            channels(0);
+            piece_mma(1);
+            channels(1);
+            channels(2);
+            piece_mma(2);
+            umma_commit(&sm.k_free[7]);                            // pieces 1 and 2
+            channels(3);
+            piece_mma(3);
+            channels(4);
+            channels(5);
+            piece_mma(4);
+            umma_commit(&sm.k_free[8]);                            // pieces 3 and 4
+            pv(std::integral_constant<int, 32>{}, 384, 384, acc);
+            umma_commit(&sm.k_free[6]);                            // and piece 0
+        }
+        umma_commit(&sm.o_full);
+        ++seg_no;
+    }
+    // every MMA of this CTA is done before tensor memory goes back
+    if (seg_no > 0) wait(&sm.o_full, (seg_no - 1) & 1u);
+}
+
+__global__ void __launch_bounds__(kGaThreads, 1)
+group_attn_kernel(const GaArgs A) {
+    extern __shared__ __align__(1024) uint8_t ga_raw[];
+    GaSmem &sm = *reinterpret_cast<GaSmem *>(ga_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.s_full, 1);
+        mbar_init(&sm.p_full, kGaSoftWarps);
+        mbar_init(&sm.d_full, 1);
+        mbar_init(&sm.d_empty, kGaSoftWarps);
+        mbar_init(&sm.o_full, 1);
+        for (int c = 0; c < kGaChunks; ++c) {
+            mbar_init(&sm.k_full[c], kGaDeqWarps);
+            mbar_init(&sm.k_free[c], 1);
+        }
+        fence_mbar_init();
+    }
+    pdl_wait();
+    ga_locate(A, sm);
+    __syncthreads();
+    const int64_t total = sm.total;
+    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    if (blockIdx.x == 0 && tid == 0) {
+        A.plan->total = total;
+        A.plan->ctas = ctas;
+    }
+    if (static_cast<int>(blockIdx.x) >= ctas) return;
+    if (tid == 0) {
+        const int64_t at = ga_range(total, blockIdx.x, ctas), local = at - sm.start;
+        const int blocks = ga_group(A, sm.start_g, false).blocks;
+        GaWalk w;
+        w.left = ga_range(total, blockIdx.x + 1, ctas) - at;
+        w.g = sm.start_g;
+        w.tile = static_cast<int>(local / blocks);
+        w.k = static_cast<int>(local - static_cast<int64_t>(w.tile) * blocks);
+        sm.walk = w;
+        GaSeg s;
+        w.next(A, s);
+        GaPlan::Tile &t = A.plan->first[blockIdx.x];
+        t.begin = at - s.k0;
+        t.blocks = s.blocks;
+        t.tok0 = s.tok0;
+        t.ntok = s.ntok;
+    }
+    if (warp == kGaMmaWarp) {
+        tmem_alloc(&sm.tmem, 512);
+        tmem_relinquish();
+        tc_fence_before();
     }
     __syncthreads();
-    for (int i = 0; i < kGaPer; ++i) {
-        const int e = i * kGaThreads + tid, h = e / kDim;
-        const int64_t at = static_cast<int64_t>(tok) * kHeads * kDim + e;
-        const float lo = A.lse_own ? A.lse_own[tok * kHeads + h] * 1.4426950408889634f : -INFINITY;
-        const float m = fmaxf(sm.m[h], lo), ref = m == -INFINITY ? 0.0f : m;
-        const float wk = exp2f(sm.m[h] - ref), wo = exp2f(lo - ref), l = sm.l[h] * wk + wo;
-        const float o = acc[i] * wk + (wo > 0.0f ? wo * A.o_own[at] : 0.0f);
-        A.out[at] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o / l);   // a NaN stays one
-        if (e % kDim == 0) A.lse[tok * kHeads + h] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+    tc_fence_after();
+    const GaWalk walk = sm.walk;
+    if (warp < kGaSoftWarps) {
+        ga_regs_up<kGaSoftRegs>();
+        ga_softmax(A, sm, walk, warp, lane);
+    } else {
+        ga_regs_down<kGaOtherRegs>();
+        if (warp < kGaMmaWarp)
+            ga_dequant(A, sm, walk, warp - kGaSoftWarps, lane);
+        else if (warp == kGaMmaWarp && lane == 0)
+            ga_mma(A, sm, walk);
     }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    pdl_trigger();
+    if (warp == kGaMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(sm.tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ K13
+// Joins the partials of the row tiles that K12's ranges cut, with the own
+// part. A unit of work is 16 channels x 16 heads of one token; 4 groups of 64
+// threads take every fourth partial each (a thread: 4 heads of one channel)
+// and are added through shared memory. HBM/L2-bound: 36,864 B per partial and
+// token.
+constexpr int kGmThreads = 256;
+constexpr int kGmCols = 16;
+constexpr int kGmUnits = kDim / kGmCols;                           // 36 per token
+
+struct GmSmem {
+    float w[kGaMaxCtas + 1][kHeads];                               // weight of a partial
+    float red[kGmThreads / kHeads][kHeads];
+    float4 sum[4][64];
+    float fo[kHeads];
+    int first[kGaMaxCtas + 1];                                     // units before the c-th boundary's tile
+    int warp_sum[kGmThreads / 32];
+};
+
+__global__ void __launch_bounds__(kGmThreads)
+group_attn_merge_kernel(const GaArgs A) {
+    __shared__ GmSmem sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t total = A.plan->total;
+    const int ctas = A.plan->ctas;
+    // The range boundary c cuts the row tile of range c's first step when the
+    // tile begins before it; the first such boundary of a tile stands for it.
+    int mine = 0;
+    if (tid > 0 && tid < ctas) {
+        const GaPlan::Tile &t = A.plan->first[tid];
+        if (t.begin < ga_range(total, tid, ctas) && t.begin >= ga_range(total, tid - 1, ctas)) mine = t.ntok * kGmUnits;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) sm.warp_sum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += sm.warp_sum[w];
+    if (tid < kGaMaxCtas) sm.first[tid + 1] = incl;
+    if (tid == 0) sm.first[0] = 0;
+    __syncthreads();
+    const int units = sm.first[kGaMaxCtas];
+    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        int lo = 0, hi = kGaMaxCtas;                               // the boundary: first[c] <= unit < first[c + 1]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (sm.first[mid] <= unit) lo = mid; else hi = mid;
+        }
+        const GaPlan::Tile t = A.plan->first[lo];
+        const int local = unit - sm.first[lo], tok = local / kGmUnits, col0 = (local - tok * kGmUnits) * kGmCols;
+        // ranges lo - 1 (which begins the tile) to the last c with total * c / ctas < the tile's end
+        const int c0 = lo - 1;
+        const int n = static_cast<int>(((t.begin + t.blocks) * ctas - 1) / total) - c0 + 1;
+        const int slot0 = 2 * c0 + (ga_range(total, c0, ctas) < t.begin ? 1 : 0);   // a range's first tile is in slot 0
+        auto slot = [&](int p) { return p == 0 ? slot0 : 2 * (c0 + p); };
+        const int h = tid & (kHeads - 1), lanes = kGmThreads / kHeads;
+        const int64_t r = static_cast<int64_t>(t.tok0 + tok) * kHeads + h;
+        const float own = A.lse_own ? __ldg(A.lse_own + r) * 1.4426950408889634f : -INFINITY;
+        float mx = own;
+        for (int p = tid >> 4; p < n; p += lanes)
+            mx = fmaxf(mx, __ldcg(&A.part_ml[(static_cast<int64_t>(slot(p)) * A.tok_slots + tok) * kHeads + h]).x);
+        sm.red[tid >> 4][h] = mx;
+        __syncthreads();
+        for (int i = 0; i < lanes; ++i) mx = fmaxf(mx, sm.red[i][h]);
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+        __syncthreads();
+        float l = 0.0f;
+        for (int p = tid >> 4; p < n; p += lanes) {
+            const float2 ml = __ldcg(&A.part_ml[(static_cast<int64_t>(slot(p)) * A.tok_slots + tok) * kHeads + h]);
+            const float w = ga_ex2(ml.x - ref);
+            sm.w[p][h] = w;
+            l += ml.y * w;
+        }
+        sm.red[tid >> 4][h] = l;
+        __syncthreads();
+        const float wo = ga_ex2(own - ref);
+        l = wo;
+        for (int i = 0; i < lanes; ++i) l += sm.red[i][h];
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;             // a NaN stays one
+        if (col0 == 0 && tid < kHeads) A.lse[r] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+        // 4 heads (hq) of one channel per thread, every fourth partial
+        const int grp = tid >> 6, col = (tid & 63) >> 2, hq = (tid & 3) * 4;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int p = grp; p < n; p += 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                A.part_o + ((static_cast<int64_t>(slot(p)) * A.tok_slots + tok) * kDim + col0 + col) * kHeads + hq));
+            a.x += sm.w[p][hq] * v.x;
+            a.y += sm.w[p][hq + 1] * v.y;
+            a.z += sm.w[p][hq + 2] * v.z;
+            a.w += sm.w[p][hq + 3] * v.w;
+        }
+        sm.sum[grp][tid & 63] = a;
+        __syncthreads();
+        // one output per thread: head tid / 16, channel tid % 16
+        const int oh = tid >> 4, oc = tid & 15;
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v += reinterpret_cast<const float *>(&sm.sum[i][oc * 4 + (oh >> 2)])[oh & 3];
+        if (tid < kHeads) {
+            sm.red[0][h] = inv;
+            sm.fo[h] = wo > 0.0f ? wo * inv : 0.0f;                // nothing to read without an own part
+        }
+        __syncthreads();
+        const int64_t at = (static_cast<int64_t>(t.tok0 + tok) * kHeads + oh) * kDim + col0 + oc;
+        v *= sm.red[0][oh];
+        if (sm.fo[oh] != 0.0f) v += sm.fo[oh] * __ldg(A.o_own + at);
+        A.out[at] = __float2bfloat16_rn(v);
+        __syncthreads();
+    }
+}
+
+// Workspace: the plan, then two partials per CTA.
+inline size_t ga_plan_bytes() { return (sizeof(GaPlan) + 255) / 256 * 256; }
+inline size_t ga_ml_bytes(int tok_slots) { return static_cast<size_t>(2 * kGaMaxCtas) * tok_slots * kHeads * sizeof(float2); }
+inline size_t ga_ws_bytes(int tok_slots) {
+    return ga_plan_bytes() + ga_ml_bytes(tok_slots) + static_cast<size_t>(2 * kGaMaxCtas) * tok_slots * kHeads * kDim * 4;
 }
 
 }  // namespace csa2

@@ -7,7 +7,10 @@ a step of the type), each probability to f16 (2^-11 of its weight: 2^-11 A),
 and a score s carries an error of at most d = 576 * 2^-24 * scale * sum |q k|
 (576 fp32 additions) plus 2^-21 |s| (the exponent's fp32 argument), which moves
 every weight by at most 2 d relatively (2 d A). f16 queries add 2^-25 of a
-row's largest magnitude per channel, covered by d. lse moves by d, by the
+row's largest magnitude per channel, covered by d. Below 2^-14 f16 has a fixed
+step of 2^-24: a probability exp(s - max) below that errs by 2^-25 absolutely
+instead (the sum they are divided by is at least 1, the largest entry's own
+probability): 2^-25 / sum times the |v| of those entries. lse moves by d, by the
 exponentials (2^-21 of each) and by the fp32 sum of T of them: positive terms,
 so each addition errs by at most 2^-24 of the final sum, and a term passes
 through at most 64 additions inside a block of 64 entries and one for each of
@@ -106,6 +109,10 @@ class Case:
             d = (576 * 2.0 ** -24 * mag + 2.0 ** -21 * s.abs())
             d = d.amax(-1) if s.shape[-1] else torch.zeros(s.shape[:2], dtype=torch.float64)
             v = k
+            low = torch.zeros(1, dtype=torch.float64)
+            if s.shape[-1]:
+                e = torch.exp(s - s.amax(-1, keepdim=True))
+                low = torch.einsum("nht,tc->nhc", (e < 2.0 ** -14).double(), v.abs()) / e.sum(-1, keepdim=True)
             if self.own is not None:
                 s = torch.cat([s, self.own[1][a:b].double()[..., None]], -1)
             m = s.amax(-1, keepdim=True) if s.shape[-1] else torch.full((b - a, H, 1), -math.inf)
@@ -120,7 +127,7 @@ class Case:
                 o = o + w[..., T:] * self.own[0][a:b].double()
                 A = A + w[..., T:] * self.own[0][a:b].double().abs()
             L = torch.where(l[..., 0] > 0, m[..., 0] + torch.log(l[..., 0].clamp(min=1e-300)), -math.inf)
-            tol = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2 * d[..., None]) * A + 1e-30
+            tol = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2 * d[..., None]) * A + 2.0 ** -25 * low + 1e-30
             err = (out[a:b] - o).abs()
             sel = slice(None) if rows is None else rows
             assert bool((err <= tol)[sel].all()), f"group {g}: off by {float((err / tol)[sel].max()):.2f} tolerances"
