@@ -63,13 +63,18 @@ constexpr int kGaChunk = 64;                                       // channels p
 constexpr int kGaChunks = kDim / kGaChunk;                         // 9
 constexpr int kGaQSlab = kGaRows * 16, kGaKSlab = kGaBlk * 16;     // 2,048 and 1,024 B: 8 channels of every row
 constexpr int kGaTmemCh = 416;                                     // channels accumulated in tensor memory
-constexpr int kGaPiece = 32;
-constexpr int kGaPieces = (kDim - kGaTmemCh) / kGaPiece;           // 5
 constexpr int kGaSCol = kGaTmemCh, kGaPCol = kGaSCol + kGaBlk;     // 416, 480
-constexpr int kGaPieceCol = kGaSCol + kGaBlk - kGaPiece;           // 448
-constexpr int kGaRegs = kGaPieces * kGaPiece / 2;                  // outputs a softmax thread holds: 80
+constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a softmax thread holds: 80
+// The chunks of a block in the order in which O's MMAs release them, so the
+// order in which they are refilled and multiplied for S; in groups with one
+// barrier each.
+constexpr int kGaGroups = 5;
+__device__ __forceinline__ constexpr int ga_order(int i) {          // 0 1 | 7 | 2 3 | 8 | 4 5 6
+    return i < 2 ? i : i == 2 ? 7 : i < 5 ? i - 1 : i == 5 ? 8 : i - 2;
+}
+__device__ __forceinline__ constexpr int ga_group_end(int g) { return g == 0 ? 2 : g == 1 ? 3 : g == 2 ? 5 : g == 3 ? 6 : 9; }
 constexpr float kGaSlack = 8.0f;                                   // log2 units a block may exceed the reference
-static_assert(kGaPCol + kGaBlk / 2 == 512, "tensor memory is full");
+static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 80, "tensor memory is full; pieces of 64, 64 and 32 channels");
 
 struct GaArgs {
     const __nv_bfloat16 *q;            // [N][16][576]
@@ -163,7 +168,7 @@ struct GaSmem {
     alignas(1024) uint8_t q[kGaRows * kDim * 2];
     alignas(1024) uint8_t k[kGaBlk * kDim * 2];
     uint64_t q_full, s_full, p_full, d_full, d_empty, o_full;
-    uint64_t k_full[kGaChunks], k_free[kGaChunks];
+    uint64_t k_full[kGaGroups], k_free[kGaGroups];
     uint32_t tmem;
     int valid[2];                      // keys of a block that count, by block parity
     float scale[kGaRows];              // a row's softmax scale (log2) times its query exponent
@@ -199,6 +204,28 @@ __device__ __forceinline__ void ga_tmem_st16(uint32_t taddr, const uint32_t (&v)
           "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 32 lanes x 32 columns.
+__device__ __forceinline__ void ga_tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ bool ga_elect() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
 }
 
 __device__ __forceinline__ float ga_ex2(float x) {
@@ -288,8 +315,9 @@ __device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaS
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
         const int eq = f16_exponent(mx);
-        const float down = exp2f(static_cast<float>(-eq));
-        if (part == 0) sm.scale[row] = A.scale_log2 * exp2f(static_cast<float>(eq));
+        // a negative softmax scale turns the query round, so that the largest score has the largest logit
+        const float down = copysignf(exp2f(static_cast<float>(-eq)), A.scale_log2);
+        if (part == 0) sm.scale[row] = fabsf(A.scale_log2) * exp2f(static_cast<float>(eq));
 #pragma unroll
         for (int u = 0; u < 18; ++u) {
             uint32_t o[4];
@@ -301,6 +329,11 @@ __device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaS
             *reinterpret_cast<uint4 *>(sm.q + (4 * u + part) * kGaQSlab + row * 16) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
+}
+
+// Channel of a softmax thread's output register i (a multiple of 16).
+__device__ __forceinline__ constexpr int ga_reg_channel(int i, int half) {
+    return i < 64 ? kGaTmemCh + (i & 32) * 2 + half * 32 + (i & 16) : kGaTmemCh + 128 + half * 16;
 }
 
 __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk walk, int warp, int lane) {
@@ -323,36 +356,41 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
         for (int kb = s.k0; kb < s.k1; ++kb, ++blk) {
             const uint32_t par = blk & 1u;
             wait(&sm.s_full, par);
-            wait(&sm.k_full[kGaChunks - 1], par);                  // orders the read of valid[] as well
+            wait(&sm.k_full[kGaGroups - 1], par);                  // orders the read of valid[] as well
             tc_fence_after();
             float x[32];
-            {
-                float a[16];
-                tmem_ld16(tm + kGaSCol + 32 * half, a);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = a[i];
-                tmem_ld16(tm + kGaSCol + 32 * half + 16, a);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[16 + i] = a[i];
-            }
+            ga_tmem_ld32(tm + kGaSCol + 32 * half, x);
             const int n = sm.valid[par] - 32 * half;
-            float mx = -INFINITY;
-            if (n >= 32) {
+            if (n < 32) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    x[i] *= scale;
-                    mx = fmaxf(mx, x[i]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    x[i] = i < n ? x[i] * scale : -INFINITY;
-                    mx = fmaxf(mx, x[i]);
-                }
+                for (int i = 0; i < 32; ++i) x[i] = i < n ? x[i] : -INFINITY;
             }
+            float mx = x[0];
+#pragma unroll
+            for (int i = 1; i < 32; ++i) mx = fmaxf(mx, x[i]);
             sm.mx[par][half][row] = mx;
+            // with the reference as it stands; again below if the block's maximum moves it
+            float sum;
+            uint32_t p[16];
+            auto exponentials = [&]() {
+                const float ref = m == -INFINITY ? 0.0f : m;
+                float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float a = ga_ex2(fmaf(x[2 * i], scale, -ref)), b = ga_ex2(fmaf(x[2 * i + 1], scale, -ref));
+                    if (n < 32) {                                  // -inf times a scale of 0
+                        a = 2 * i < n ? a : 0.0f;
+                        b = 2 * i + 1 < n ? b : 0.0f;
+                    }
+                    s4[i & 3] += a + b;
+                    p[i] = f32x2_f16x2(a, b);
+                }
+                sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            };
+            exponentials();
             ga_pair_bar(pair_bar);
             mx = fmaxf(mx, sm.mx[par][half ^ 1][row]);
+            mx = mx == -INFINITY ? mx : mx * scale;
             const bool raise = mx > m + kGaSlack || (m == -INFINITY && mx > m);
             if (__any_sync(0xffffffffu, raise)) {
                 const float f = raise ? ga_ex2(m - mx) : 1.0f;     // 0 for the first keys of a row
@@ -372,34 +410,31 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
                         ga_tmem_st16(at, o);
                     }
                 }
-            }
-            const float ref = m == -INFINITY ? 0.0f : m;
-            float sum = 0.0f;
-            uint32_t p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float a = ga_ex2(x[2 * i] - ref), b = ga_ex2(x[2 * i + 1] - ref);
-                sum += a + b;
-                p[i] = f32x2_f16x2(a, b);
+                exponentials();
             }
             l += sum;
             ga_tmem_st16(tm + kGaPCol + 16 * half, p);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_full);
-            // the 32-channel pieces of this block
-#pragma unroll
-            for (int j = 0; j < kGaPieces; ++j, ++piece) {
+            // the block's pieces of 64, 64 and 32 channels: this half's columns
+            auto piece_add = [&](auto n_, int to) {
+                constexpr int kN = decltype(n_)::value;            // columns of this half
                 wait(&sm.d_full, piece & 1u);
+                ++piece;
                 tc_fence_after();
-                float a[16];
-                tmem_ld16(tm + kGaPieceCol + 16 * half, a);
+                float a[kN];
+                if constexpr (kN == 32) ga_tmem_ld32(tm + kGaSCol + 32 * half, a);
+                else tmem_ld16(tm + kGaSCol + 16 * half, a);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.d_empty);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[j * 16 + i] += a[i];
-            }
+                for (int i = 0; i < kN; ++i) acc[to + i] += a[i];
+            };
+            piece_add(std::integral_constant<int, 32>{}, 0);
+            piece_add(std::integral_constant<int, 32>{}, 32);
+            piece_add(std::integral_constant<int, 16>{}, 64);
         }
         // ---- end of the segment
         wait(&sm.o_full, seg_no & 1u);
@@ -426,8 +461,7 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
             }
             if (live)
 #pragma unroll
-                for (int i = 0; i < kGaRegs; ++i)
-                    po[(kGaTmemCh + (i >> 4) * kGaPiece + half * 16 + (i & 15)) * kHeads] = acc[i];
+                for (int i = 0; i < kGaRegs; ++i) po[(ga_reg_channel(i & ~15, half) + (i & 15)) * kHeads] = acc[i];
         } else {
             // the whole row tile: join the token's own part and write it
             const int64_t r = static_cast<int64_t>(s.tok0 + (live ? tok : 0)) * kHeads + h;
@@ -472,7 +506,7 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
             }
             if (live)
 #pragma unroll
-                for (int j = 0; j < kGaPieces; ++j) write(kGaTmemCh + j * kGaPiece + half * 16, acc + 16 * j);
+                for (int j = 0; j < kGaRegs; j += 16) write(ga_reg_channel(j, half), acc + j);
         }
         tc_fence_before();
         ++seg_no;
@@ -524,27 +558,41 @@ __device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk w
         }
         if (more) open();
 #pragma unroll
-        for (int c = 0; c < kGaChunks; ++c) {
-            if (blk > 0) wait(&sm.k_free[c], (blk - 1) & 1u);
-            const uint32_t s2 = e4m3x2_to_f16x2(sc[c]);
-            const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
+        for (int g = 0; g < kGaGroups; ++g) {
+            if (blk > 0) wait(&sm.k_free[g], (blk - 1) & 1u);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const uint32_t w = (&raw[c].x)[u], f = u < 2 ? sa : sb;
-                *reinterpret_cast<uint4 *>(sm.k + (8 * c + 4 * part + u) * kGaKSlab + key * 16) =
-                    make_uint4(hmul2_u32(e2m1x2_to_f16x2(w & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2((w >> 8) & 0xffu), f),
-                               hmul2_u32(e2m1x2_to_f16x2((w >> 16) & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2(w >> 24), f));
+            for (int i = g == 0 ? 0 : ga_group_end(g - 1); i < ga_group_end(g); ++i) {
+                const int c = ga_order(i);
+                const uint32_t s2 = e4m3x2_to_f16x2(sc[c]);
+                const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t w = (&raw[c].x)[u], f = u < 2 ? sa : sb;
+                    *reinterpret_cast<uint4 *>(sm.k + (8 * c + 4 * part + u) * kGaKSlab + key * 16) =
+                        make_uint4(hmul2_u32(e2m1x2_to_f16x2(w & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2((w >> 8) & 0xffu), f),
+                                   hmul2_u32(e2m1x2_to_f16x2((w >> 16) & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2(w >> 24), f));
+                }
+                if (more) load(c);                                 // in flight until the next block's turn
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.k_full[c]);
-            if (more) load(c);                                     // in flight until the next block's turn
+            if (lane == 0) mbar_arrive(&sm.k_full[g]);
         }
     }
 }
 
+// The whole warp walks and waits; one elected thread issues. Offsets and shapes
+// are compile-time constants (run-time descriptors double an MMA's issue time)
+// and the tensor memory address is 0: all of it is allocated.
+template <int kN, int kCh, int kCol>
+__device__ __forceinline__ void ga_pv(uint64_t d_v, uint32_t accumulate) {
+    constexpr uint32_t id = umma_idesc(kGaRows, kN, false, true);
+#pragma unroll
+    for (int j = 0; j < kGaBlk / 16; ++j)
+        ga_mma_ts(kCol, kGaPCol + 8 * j, d_v + ((kCh / 8 * kGaKSlab + j * 256) >> 4), id, j > 0 ? 1u : accumulate);
+}
+
 __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk) {
-    const uint32_t tm = sm.tmem;
     // K-major: leading offset along K (8 channels), stride offset along the rows; MN-major: along the keys, along the channels
     const uint64_t d_q = umma_desc(smem_u32(sm.q), kGaQSlab, 128, 0);
     const uint64_t d_k = umma_desc(smem_u32(sm.k), kGaKSlab, 128, 0);
@@ -557,56 +605,58 @@ __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk)
         wait(&sm.q_full, seg_no & 1u);
         for (int kb = s.k0; kb < s.k1; ++kb, ++blk) {
             const uint32_t par = blk & 1u, acc = kb > s.k0;
-            // S: the last piece of the block before has been read (it lies in S's columns)
+            // S takes the columns of the pieces: the last one has been read
             if (piece > 0) wait(&sm.d_empty, (piece - 1) & 1u);
             tc_fence_after();
-            for (int c = 0; c < kGaChunks; ++c) {
-                wait(&sm.k_full[c], par);
 #pragma unroll
-                for (int j = 0; j < kGaChunk / 16; ++j)
-                    ga_mma_ss(tm + kGaSCol, d_q + ((c * 8 + j * 2) * kGaQSlab >> 4), d_k + ((c * 8 + j * 2) * kGaKSlab >> 4),
-                              id_qk, (c | j) != 0);
+            for (int g = 0; g < kGaGroups; ++g) {
+                wait(&sm.k_full[g], par);
+                if (ga_elect()) {
+#pragma unroll
+                    for (int i = g == 0 ? 0 : ga_group_end(g - 1); i < ga_group_end(g); ++i)
+#pragma unroll
+                        for (int j = 0; j < kGaChunk / 16; ++j)
+                            ga_mma_ss(kGaSCol, d_q + ((ga_order(i) * 8 + j * 2) * kGaQSlab >> 4),
+                                      d_k + ((ga_order(i) * 8 + j * 2) * kGaKSlab >> 4), id_qk, i > 0 || j > 0);
+                    if (g == kGaGroups - 1) umma_commit(&sm.s_full);
+                }
+                __syncwarp();
             }
-            umma_commit(&sm.s_full);
             wait(&sm.p_full, par);
             tc_fence_after();
-            // channels [ch, ch + N) of O or of a piece, K = 64 keys
-            auto pv = [&](auto n, int ch, uint32_t d, uint32_t a) {
-                constexpr uint32_t id = umma_idesc(kGaRows, decltype(n)::value, false, true);
-#pragma unroll
-                for (int j = 0; j < kGaBlk / 16; ++j)
-                    ga_mma_ts(tm + d, tm + kGaPCol + 8 * j, d_v + ((ch / 8 * kGaKSlab + j * 256) >> 4), id, a | (j > 0));
-            };
-            auto channels = [&](int c) {
-                pv(std::integral_constant<int, 64>{}, 64 * c, 64 * c, acc);
-                umma_commit(&sm.k_free[c]);
-            };
-            auto piece_mma = [&](int j) {
-                if (j > 0) {
-                    wait(&sm.d_empty, (piece - 1) & 1u);
-                    tc_fence_after();
-                }
-                pv(std::integral_constant<int, kGaPiece>{}, kGaTmemCh + kGaPiece * j, kGaPieceCol, 0u);
+            // O in parts of 128, 128 and 160 channels between the pieces of 64, 64 and 32 (channels 416, 480 and
+            // 544 on), so that a piece is read while a part is multiplied
+            if (ga_elect()) {
+                ga_pv<64, 416, kGaSCol>(d_v, 0u);
                 umma_commit(&sm.d_full);
-                ++piece;
-            };
-            piece_mma(0);
-            channels(0);
-            piece_mma(1);
-            channels(1);
-            channels(2);
-            piece_mma(2);
-            umma_commit(&sm.k_free[7]);                            // pieces 1 and 2
-            channels(3);
-            piece_mma(3);
-            channels(4);
-            channels(5);
-            piece_mma(4);
-            umma_commit(&sm.k_free[8]);                            // pieces 3 and 4
-            pv(std::integral_constant<int, 32>{}, 384, 384, acc);
-            umma_commit(&sm.k_free[6]);                            // and piece 0
+                ga_pv<128, 0, 0>(d_v, acc);
+                umma_commit(&sm.k_free[0]);                        // chunks 0, 1
+            }
+            __syncwarp();
+            wait(&sm.d_empty, piece & 1u);
+            tc_fence_after();
+            if (ga_elect()) {
+                ga_pv<64, 480, kGaSCol>(d_v, 0u);
+                umma_commit(&sm.d_full);
+                umma_commit(&sm.k_free[1]);                        // chunk 7
+                ga_pv<128, 128, 128>(d_v, acc);
+                umma_commit(&sm.k_free[2]);                        // chunks 2, 3
+            }
+            __syncwarp();
+            wait(&sm.d_empty, (piece + 1) & 1u);
+            tc_fence_after();
+            if (ga_elect()) {
+                ga_pv<32, 544, kGaSCol>(d_v, 0u);
+                umma_commit(&sm.d_full);
+                umma_commit(&sm.k_free[3]);                        // chunk 8
+                ga_pv<160, 256, 256>(d_v, acc);
+                umma_commit(&sm.k_free[4]);                        // chunks 4, 5, 6
+            }
+            __syncwarp();
+            piece += 3;
         }
-        umma_commit(&sm.o_full);
+        if (ga_elect()) umma_commit(&sm.o_full);
+        __syncwarp();
         ++seg_no;
     }
     // every MMA of this CTA is done before tensor memory goes back
@@ -625,7 +675,7 @@ group_attn_kernel(const GaArgs A) {
         mbar_init(&sm.d_full, 1);
         mbar_init(&sm.d_empty, kGaSoftWarps);
         mbar_init(&sm.o_full, 1);
-        for (int c = 0; c < kGaChunks; ++c) {
+        for (int c = 0; c < kGaGroups; ++c) {
             mbar_init(&sm.k_full[c], kGaDeqWarps);
             mbar_init(&sm.k_free[c], 1);
         }
@@ -673,7 +723,7 @@ group_attn_kernel(const GaArgs A) {
         ga_regs_down<kGaOtherRegs>();
         if (warp < kGaMmaWarp)
             ga_dequant(A, sm, walk, warp - kGaSoftWarps, lane);
-        else if (warp == kGaMmaWarp && lane == 0)
+        else if (warp == kGaMmaWarp)
             ga_mma(A, sm, walk);
     }
     __syncwarp();
