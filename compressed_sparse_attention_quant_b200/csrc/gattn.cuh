@@ -73,6 +73,7 @@ __device__ __forceinline__ constexpr int ga_order(int i) {          // 0 1 | 7 |
     return i < 2 ? i : i == 2 ? 7 : i < 5 ? i - 1 : i == 5 ? 8 : i - 2;
 }
 __device__ __forceinline__ constexpr int ga_group_end(int g) { return g == 0 ? 2 : g == 1 ? 3 : g == 2 ? 5 : g == 3 ? 6 : 9; }
+constexpr int kGaGap = 2;                                          // steps a row tile counts for beside its blocks
 constexpr float kGaSlack = 8.0f;                                   // log2 units a block may exceed the reference
 static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 80, "tensor memory is full; pieces of 64, 64 and 32 channels");
 
@@ -99,7 +100,8 @@ struct GaArgs {
 struct GaPlan {
     int64_t total;                     // steps of all row tiles
     int ctas;                          // ranges
-    struct Tile { int64_t begin; int blocks, tok0, ntok; } first[kGaMaxCtas];   // row tile of a range's first step
+    // row tile of a range's first step; begin is the step of its first block
+    struct Tile { int64_t begin; int blocks, tok0, ntok; } first[kGaMaxCtas];
 };
 
 __host__ __device__ __forceinline__ int64_t ga_range(int64_t total, int c, int ctas) { return total * c / ctas; }
@@ -129,8 +131,11 @@ __device__ __forceinline__ GaGroup ga_group(const GaArgs &A, int g, bool report)
     return r;
 }
 
+// A row tile's steps: its blocks, after kGaGap steps that stand for what it
+// costs besides (query in, result out), so that ranges with many short tiles
+// are not the longest.
 __device__ __forceinline__ int64_t ga_steps(const GaGroup &g) {
-    return static_cast<int64_t>((g.n + kGaTok - 1) / kGaTok) * g.blocks;
+    return static_cast<int64_t>((g.n + kGaTok - 1) / kGaTok) * (kGaGap + g.blocks);
 }
 
 // One row tile's blocks [k0, k1) of a CTA's range.
@@ -141,26 +146,29 @@ struct GaSeg {
 // Walks a range segment by segment; every role of the CTA does so by itself.
 struct GaWalk {
     int64_t left;                      // steps to go
-    int g, tile, k;                    // group, row tile of the group, block of the row tile
+    int g, tile, k;                    // group, row tile of the group, step of the row tile
     __device__ __forceinline__ bool next(const GaArgs &A, GaSeg &s) {
-        if (left <= 0) return false;
-        GaGroup grp = ga_group(A, g, false);
-        while (tile * kGaTok >= grp.n) {
-            if (++g >= A.G) return false;
-            grp = ga_group(A, g, false);
-            tile = 0;
+        while (left > 0) {
+            GaGroup grp = ga_group(A, g, false);
+            while (tile * kGaTok >= grp.n) {
+                if (++g >= A.G) return false;
+                grp = ga_group(A, g, false);
+                tile = 0;
+            }
+            const int len = kGaGap + grp.blocks, end = left < len - k ? k + static_cast<int>(left) : len;
+            s.g = g;
+            s.tok0 = grp.tok0 + tile * kGaTok;
+            s.ntok = min(kGaTok, grp.n - tile * kGaTok);
+            s.T = grp.T;
+            s.blocks = grp.blocks;
+            s.k0 = max(0, k - kGaGap);
+            s.k1 = max(0, end - kGaGap);
+            left -= end - k;
+            k = 0;
+            ++tile;
+            if (s.k1 > s.k0) return true;
         }
-        s.g = g;
-        s.tok0 = grp.tok0 + tile * kGaTok;
-        s.ntok = min(kGaTok, grp.n - tile * kGaTok);
-        s.T = grp.T;
-        s.blocks = grp.blocks;
-        s.k0 = k;
-        s.k1 = left < grp.blocks - k ? k + static_cast<int>(left) : grp.blocks;
-        left -= s.k1 - s.k0;
-        k = 0;
-        ++tile;
-        return true;
+        return false;
     }
 };
 
@@ -250,83 +258,102 @@ struct GaWait {
 };
 
 // ---------------------------------------------------------------- roles
-// The first step of this CTA's range: its group, and the totals.
+// The first step of this CTA's range (its group, and that group's first step)
+// and the total: a block scan over the groups, again over the chunks of 512
+// when there are more.
 __device__ __forceinline__ void ga_locate(const GaArgs &A, GaSmem &sm) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kWarps = kGaThreads / 32;
-    int64_t mine = 0, total = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        int64_t base = 0, begin = 0, want = -1;
-        int ctas = 0;
-        if (pass == 1) {
-            ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-            want = static_cast<int>(blockIdx.x) < ctas ? ga_range(total, blockIdx.x, ctas) : -1;
-            if (tid == 0) {
-                sm.total = total;
-                sm.start_g = -1;
-            }
-        }
-        for (int g0 = 0; g0 < A.G; g0 += kGaThreads) {
-            if (pass == 0 || A.G > kGaThreads)            // one chunk of groups is scanned from registers
-                mine = g0 + tid < A.G ? ga_steps(ga_group(A, g0 + tid, pass == 0 && blockIdx.x == 0)) : 0;
-            int64_t incl = mine;
+    int64_t base = 0, begin = 0, mine = 0;
+    auto scan = [&](int g0, bool report) {                // begin, mine of group g0 + tid; base moves past the chunk
+        mine = g0 + tid < A.G ? ga_steps(ga_group(A, g0 + tid, report)) : 0;
+        int64_t incl = mine;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += o;
-            }
-            if (lane == 31) sm.scan[warp] = incl;
-            __syncthreads();
-            int64_t all = 0, before = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) before += sm.scan[w];
-                all += sm.scan[w];
-            }
-            begin = base + before + incl - mine;
-            if (want >= begin && want < begin + mine) {
-                sm.start_g = g0 + tid;
-                sm.start = begin;
-            }
-            base += all;
-            __syncthreads();
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
         }
-        total = base;
+        if (lane == 31) sm.scan[warp] = incl;
+        __syncthreads();
+        begin = base + incl - mine;
+#pragma unroll 1
+        for (int w = 0; w < kWarps; ++w) {
+            const int64_t v = sm.scan[w];
+            if (w < warp) begin += v;
+            base += v;
+        }
+        __syncthreads();
+    };
+    for (int g0 = 0; g0 < A.G; g0 += kGaThreads) scan(g0, blockIdx.x == 0);
+    const int64_t total = base;
+    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    const int64_t want = static_cast<int>(blockIdx.x) < ctas ? ga_range(total, blockIdx.x, ctas) : -1;
+    if (tid == 0) sm.total = total;
+    base = 0;
+    for (int g0 = 0; g0 < A.G; g0 += kGaThreads) {
+        if (A.G > kGaThreads) scan(g0, false);
+        if (want >= begin && want < begin + mine) {
+            sm.start_g = g0 + tid;
+            sm.start = begin;
+        }
     }
 }
 
-// Query tile -> f16 under a power-of-two exponent per row, one token per warp.
+// Query tile -> f16 under a power-of-two exponent per row, one token per warp:
+// a warp's loads are 64-byte runs of 8 rows and its stores whole 128-byte core
+// matrices. The exponent is 0 as a rule, so the rows are stored as they come
+// and again only where the largest magnitude asks for another one. Kept small:
+// the code runs once per row tile, at the pace of the instruction fetch.
 __device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaSeg &s, int warp, int lane) {
+    const bool some = warp < s.ntok;
+    // a negative softmax scale turns the query round, so that the largest score has the largest logit
+    const float sign = copysignf(1.0f, A.scale_log2);
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
         const int h = half * 8 + (lane & 7), row = warp * kHeads + h, part = lane >> 3;
-        uint4 v[18];
-        float mx = 0.0f;
-        const bool some = warp < s.ntok;
-        const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (static_cast<int64_t>(s.tok0 + (some ? warp : 0)) * kHeads + h) * kDim);
+        const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (static_cast<int64_t>(s.tok0 + (some ? warp : 0)) * kHeads + h) * kDim) + part;
+        uint8_t *dst = sm.q + part * kGaQSlab + row * 16;
+        float mx = 0.0f, down = sign;
+        for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+            for (int u0 = 0; u0 < 18; u0 += 9) {
+                uint4 v[9];
 #pragma unroll
-        for (int u = 0; u < 18; ++u) v[u] = some ? __ldg(src + 4 * u + part) : make_uint4(0u, 0u, 0u, 0u);
+                for (int u = 0; u < 9; ++u) v[u] = some ? __ldg(src + 4 * (u0 + u)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int u = 0; u < 18; ++u)
+                for (int u = 0; u < 9; ++u) {
+                    uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = bf16x2_f32((&v[u].x)[e]);
-                mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = bf16x2_f32((&v[u].x)[e]);
+                        mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        o[e] = f32x2_f16x2(f.x * down, f.y * down);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + 4 * (u0 + u) * kGaQSlab) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
             }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const int eq = f16_exponent(mx);
-        // a negative softmax scale turns the query round, so that the largest score has the largest logit
-        const float down = copysignf(exp2f(static_cast<float>(-eq)), A.scale_log2);
-        if (part == 0) sm.scale[row] = fabsf(A.scale_log2) * exp2f(static_cast<float>(eq));
-#pragma unroll
-        for (int u = 0; u < 18; ++u) {
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = bf16x2_f32((&v[u].x)[e]);
-                o[e] = f32x2_f16x2(f.x * down, f.y * down);
-            }
-            *reinterpret_cast<uint4 *>(sm.q + (4 * u + part) * kGaQSlab + row * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const int eq = f16_exponent(mx);
+            if (part == 0) sm.scale[row] = fabsf(A.scale_log2) * exp2f(static_cast<float>(eq));
+            if (!__any_sync(0xffffffffu, eq != 0)) break;
+            down = sign * exp2f(static_cast<float>(-eq));
+        }
+    }
+}
+
+// A segment of a group without entries: its tokens' own parts, or zeros.
+__device__ __forceinline__ void ga_own_only(const GaArgs &A, const GaSeg &s, int warp, int lane) {
+    if (warp >= s.ntok) return;
+#pragma unroll 1
+    for (int h = 0; h < kHeads; ++h) {
+        const int64_t r = static_cast<int64_t>(s.tok0 + warp) * kHeads + h;
+        const float own = A.lse_own ? __ldg(A.lse_own + r) : -INFINITY;
+        if (lane == 0) A.lse[r] = own;
+        for (int c = lane * 2; c < kDim; c += 64) {
+            float2 v = make_float2(0.0f, 0.0f);
+            if (own != -INFINITY) v = __ldg(reinterpret_cast<const float2 *>(A.o_own + r * kDim + c));
+            *reinterpret_cast<__nv_bfloat162 *>(A.out + r * kDim + c) = __floats2bfloat162_rn(v.x, v.y);
         }
     }
 }
@@ -341,9 +368,14 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
     const uint32_t tm = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int pair_bar = 1 + (warp & 3);                           // the two warps of the same rows
     GaWait wait;
-    uint32_t blk = 0, piece = 0, seg_no = 0;
+    uint32_t blk = 0, piece = 0, seg_no = 0, tile_no = 0;          // tile_no: segments with entries
     GaSeg s;
     while (walk.next(A, s)) {
+        if (s.T == 0) {
+            ga_own_only(A, s, warp, lane);
+            ++seg_no;
+            continue;
+        }
         ga_load_q(A, sm, s, warp, lane);
         fence_proxy_async_smem();
         asm volatile("bar.sync 5, 256;" ::: "memory");             // scales of all rows; the tile is whole
@@ -437,7 +469,7 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
             piece_add(std::integral_constant<int, 16>{}, 64);
         }
         // ---- end of the segment
-        wait(&sm.o_full, seg_no & 1u);
+        wait(&sm.o_full, tile_no & 1u);
         tc_fence_after();
         const int tok = row >> 4, h = row & 15;
         const bool live = tok < s.ntok;
@@ -510,6 +542,7 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
         }
         tc_fence_before();
         ++seg_no;
+        ++tile_no;
     }
 }
 
@@ -543,7 +576,13 @@ __device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk w
         raw[c] = ok ? __ldg(codes + 2 * c) : make_uint4(0u, 0u, 0u, 0u);
         sc[c] = ok ? __ldg(scales + 2 * c) : 0u;
     };
-    bool more = walk.next(A, s);
+    auto advance = [&]() {                                         // the next segment with entries
+        do {
+            if (!walk.next(A, s)) return false;
+        } while (s.T == 0);
+        return true;
+    };
+    bool more = advance();
     if (more) {
         kb = s.k0;
         open();
@@ -553,7 +592,7 @@ __device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk w
     for (uint32_t blk = 0; more; ++blk) {
         if (warp == 0 && lane == 0) sm.valid[blk & 1u] = n;
         if (++kb == s.k1) {                                        // the block after
-            more = walk.next(A, s);
+            more = advance();
             kb = s.k0;
         }
         if (more) open();
@@ -602,6 +641,7 @@ __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk)
     uint32_t blk = 0, piece = 0, seg_no = 0;
     GaSeg s;
     while (walk.next(A, s)) {
+        if (s.T == 0) continue;
         wait(&sm.q_full, seg_no & 1u);
         for (int kb = s.k0; kb < s.k1; ++kb, ++blk) {
             const uint32_t par = blk & 1u, acc = kb > s.k0;
@@ -693,20 +733,19 @@ group_attn_kernel(const GaArgs A) {
     if (static_cast<int>(blockIdx.x) >= ctas) return;
     if (tid == 0) {
         const int64_t at = ga_range(total, blockIdx.x, ctas), local = at - sm.start;
-        const int blocks = ga_group(A, sm.start_g, false).blocks;
+        const GaGroup grp = ga_group(A, sm.start_g, false);
+        const int len = kGaGap + grp.blocks;
         GaWalk w;
         w.left = ga_range(total, blockIdx.x + 1, ctas) - at;
         w.g = sm.start_g;
-        w.tile = static_cast<int>(local / blocks);
-        w.k = static_cast<int>(local - static_cast<int64_t>(w.tile) * blocks);
+        w.tile = static_cast<int>(local / len);
+        w.k = static_cast<int>(local - static_cast<int64_t>(w.tile) * len);
         sm.walk = w;
-        GaSeg s;
-        w.next(A, s);
         GaPlan::Tile &t = A.plan->first[blockIdx.x];
-        t.begin = at - s.k0;
-        t.blocks = s.blocks;
-        t.tok0 = s.tok0;
-        t.ntok = s.ntok;
+        t.begin = at - w.k + kGaGap;
+        t.blocks = grp.blocks;
+        t.tok0 = grp.tok0 + w.tile * kGaTok;
+        t.ntok = min(kGaTok, grp.n - w.tile * kGaTok);
     }
     if (warp == kGaMmaWarp) {
         tmem_alloc(&sm.tmem, 512);
@@ -738,24 +777,142 @@ group_attn_kernel(const GaArgs A) {
 
 // ------------------------------------------------------------------ K13
 // Joins the partials of the row tiles that K12's ranges cut, with the own
-// part. A unit of work is 16 channels x 16 heads of one token; 4 groups of 64
-// threads take every fourth partial each (a thread: 4 heads of one channel)
-// and are added through shared memory. HBM/L2-bound: 36,864 B per partial and
-// token.
+// part. Memory-bound in principle (36,864 B per partial and token, L2), latency
+// bound per unit of work, so a unit is one slice of a token's channels: all
+// 576, 64 or 16 of them, the smaller the fewer tokens there are to fill the
+// GPU. A thread takes 4 heads of a channel; with 16 channels the four groups of
+// 64 threads take every fourth partial each.
 constexpr int kGmThreads = 256;
-constexpr int kGmCols = 16;
-constexpr int kGmUnits = kDim / kGmCols;                           // 36 per token
 
 struct GmSmem {
     float w[kGaMaxCtas + 1][kHeads];                               // weight of a partial
     float red[kGmThreads / kHeads][kHeads];
-    float4 sum[4][64];
-    float fo[kHeads];
+    union {
+        float4 sum[4][64];
+        alignas(16) uint16_t out[kHeads][kDim + 8];
+    };
+    float inv[kHeads], fo[kHeads];
     int first[kGaMaxCtas + 1];                                     // units before the c-th boundary's tile
     int warp_sum[kGmThreads / 32];
 };
 
-__global__ void __launch_bounds__(kGmThreads)
+// The token's weights: of partial p for head h in sm.w, of the own part in sm.fo.
+struct GmTile {
+    int n, slot0, c0;                                              // partials; the first one's slot; its range
+    __device__ __forceinline__ int slot(int p) const { return p == 0 ? slot0 : 2 * (c0 + p); }
+};
+
+__device__ __forceinline__ void gm_weights(const GaArgs &A, GmSmem &sm, const GmTile &t, int tok, int64_t row, bool first) {
+    const int tid = threadIdx.x, h = tid & (kHeads - 1), at = tid >> 4;
+    constexpr int kLanes = kGmThreads / kHeads, kMost = (kGaMaxCtas + kLanes) / kLanes;
+    float2 ml[kMost];
+    float own = -INFINITY;
+    if (A.lse_own) own = __ldg(A.lse_own + row + h) * 1.4426950408889634f;
+    float mx = own;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int p = at + i * kLanes;
+        ml[i] = make_float2(-INFINITY, 0.0f);
+        if (p < t.n) ml[i] = __ldcg(&A.part_ml[(static_cast<int64_t>(t.slot(p)) * A.tok_slots + tok) * kHeads + h]);
+    }
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) mx = fmaxf(mx, ml[i].x);
+    sm.red[at][h] = mx;
+    __syncthreads();
+    for (int i = 0; i < kLanes; ++i) mx = fmaxf(mx, sm.red[i][h]);
+    const float ref = mx == -INFINITY ? 0.0f : mx;
+    __syncthreads();
+    float l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int p = at + i * kLanes;
+        if (p < t.n) {
+            const float w = ga_ex2(ml[i].x - ref);
+            sm.w[p][h] = w;
+            l += ml[i].y * w;
+        }
+    }
+    sm.red[at][h] = l;
+    __syncthreads();
+    if (tid < kHeads) {
+        const float wo = ga_ex2(own - ref);
+        l = wo;
+        for (int i = 0; i < kLanes; ++i) l += sm.red[i][h];
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;             // a NaN stays one
+        sm.inv[h] = inv;
+        sm.fo[h] = wo > 0.0f ? wo * inv : 0.0f;                    // nothing to read without an own part
+        if (first) A.lse[row + h] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+    }
+    __syncthreads();
+}
+
+// kPer x 64 channels of a token from col0 on.
+template <int kPer>
+__device__ __forceinline__ void gm_slice(const GaArgs &A, GmSmem &sm, const GmTile &t, int tok, int64_t row, int col0) {
+    const int tid = threadIdx.x, hq = (tid & 3) * 4, col = col0 + (tid >> 2);
+    float4 a[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) a[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll (kPer == 1 ? 8 : 1)
+    for (int p = 0; p < t.n; ++p) {
+        const float4 *src = reinterpret_cast<const float4 *>(
+            A.part_o + ((static_cast<int64_t>(t.slot(p)) * A.tok_slots + tok) * kDim + col) * kHeads + hq);
+        const float4 w = *reinterpret_cast<const float4 *>(&sm.w[p][hq]);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const float4 v = __ldcg(src + i * (64 * kHeads / 4));
+            a[i].x += w.x * v.x;
+            a[i].y += w.y * v.y;
+            a[i].z += w.z * v.z;
+            a[i].w += w.w * v.w;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int h = hq + e, c = col + 64 * i;
+            float v = (&a[i].x)[e] * sm.inv[h];
+            if (sm.fo[h] != 0.0f) v += sm.fo[h] * __ldg(A.o_own + (row + h) * kDim + c);
+            const __nv_bfloat16 b = __float2bfloat16_rn(v);
+            sm.out[h][c - col0] = *reinterpret_cast<const uint16_t *>(&b);
+        }
+    __syncthreads();
+    for (int i = tid; i < kHeads * kPer * 8; i += kGmThreads) {    // 8 channels each
+        const int h = i / (kPer * 8), c = i % (kPer * 8) * 8;
+        *reinterpret_cast<uint4 *>(A.out + (row + h) * kDim + col0 + c) = *reinterpret_cast<const uint4 *>(&sm.out[h][c]);
+    }
+    __syncthreads();
+}
+
+// 16 channels of a token from col0 on.
+__device__ __forceinline__ void gm_slice16(const GaArgs &A, GmSmem &sm, const GmTile &t, int tok, int64_t row, int col0) {
+    const int tid = threadIdx.x, grp = tid >> 6, col = (tid & 63) >> 2, hq = (tid & 3) * 4;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int p = grp; p < t.n; p += 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+            A.part_o + ((static_cast<int64_t>(t.slot(p)) * A.tok_slots + tok) * kDim + col0 + col) * kHeads + hq));
+        const float4 w = *reinterpret_cast<const float4 *>(&sm.w[p][hq]);
+        a.x += w.x * v.x;
+        a.y += w.y * v.y;
+        a.z += w.z * v.z;
+        a.w += w.w * v.w;
+    }
+    sm.sum[grp][tid & 63] = a;
+    __syncthreads();
+    const int h = tid >> 4, c = tid & 15;                          // one output per thread
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v += reinterpret_cast<const float *>(&sm.sum[i][c * 4 + (h >> 2)])[h & 3];
+    const int64_t at = (row + h) * kDim + col0 + c;
+    v *= sm.inv[h];
+    if (sm.fo[h] != 0.0f) v += sm.fo[h] * __ldg(A.o_own + at);
+    A.out[at] = __float2bfloat16_rn(v);
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kGmThreads, 4)
 group_attn_merge_kernel(const GaArgs A) {
     __shared__ GmSmem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -768,7 +925,7 @@ group_attn_merge_kernel(const GaArgs A) {
     int mine = 0;
     if (tid > 0 && tid < ctas) {
         const GaPlan::Tile &t = A.plan->first[tid];
-        if (t.begin < ga_range(total, tid, ctas) && t.begin >= ga_range(total, tid - 1, ctas)) mine = t.ntok * kGmUnits;
+        if (t.begin < ga_range(total, tid, ctas) && t.begin >= ga_range(total, tid - 1, ctas)) mine = t.ntok;
     }
     int incl = mine;
 #pragma unroll
@@ -779,77 +936,32 @@ group_attn_merge_kernel(const GaArgs A) {
     if (lane == 31) sm.warp_sum[warp] = incl;
     __syncthreads();
     for (int w = 0; w < warp; ++w) incl += sm.warp_sum[w];
-    if (tid < kGaMaxCtas) sm.first[tid + 1] = incl;
+    if (tid < kGaMaxCtas) sm.first[tid + 1] = incl;                // tokens up to boundary tid
     if (tid == 0) sm.first[0] = 0;
     __syncthreads();
-    const int units = sm.first[kGaMaxCtas];
-    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        int lo = 0, hi = kGaMaxCtas;                               // the boundary: first[c] <= unit < first[c + 1]
+    const int tokens = sm.first[kGaMaxCtas];
+    // slices of 16 channels while 36 of them per token fit one wave of CTAs, then of 64, then whole tokens
+    const int grid = static_cast<int>(gridDim.x);
+    const int per = tokens * 36 <= grid ? 36 : tokens * 9 <= 2 * grid ? 9 : 1;
+    for (int unit = blockIdx.x; unit < tokens * per; unit += grid) {
+        const int ut = unit / per, slice = unit - ut * per;
+        int lo = 0, hi = kGaMaxCtas;                               // the boundary: first[c] <= ut < first[c + 1]
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (sm.first[mid] <= unit) lo = mid; else hi = mid;
+            if (sm.first[mid] <= ut) lo = mid; else hi = mid;
         }
-        const GaPlan::Tile t = A.plan->first[lo];
-        const int local = unit - sm.first[lo], tok = local / kGmUnits, col0 = (local - tok * kGmUnits) * kGmCols;
+        const GaPlan::Tile tile = A.plan->first[lo];
+        const int tok = ut - sm.first[lo];
         // ranges lo - 1 (which begins the tile) to the last c with total * c / ctas < the tile's end
-        const int c0 = lo - 1;
-        const int n = static_cast<int>(((t.begin + t.blocks) * ctas - 1) / total) - c0 + 1;
-        const int slot0 = 2 * c0 + (ga_range(total, c0, ctas) < t.begin ? 1 : 0);   // a range's first tile is in slot 0
-        auto slot = [&](int p) { return p == 0 ? slot0 : 2 * (c0 + p); };
-        const int h = tid & (kHeads - 1), lanes = kGmThreads / kHeads;
-        const int64_t r = static_cast<int64_t>(t.tok0 + tok) * kHeads + h;
-        const float own = A.lse_own ? __ldg(A.lse_own + r) * 1.4426950408889634f : -INFINITY;
-        float mx = own;
-        for (int p = tid >> 4; p < n; p += lanes)
-            mx = fmaxf(mx, __ldcg(&A.part_ml[(static_cast<int64_t>(slot(p)) * A.tok_slots + tok) * kHeads + h]).x);
-        sm.red[tid >> 4][h] = mx;
-        __syncthreads();
-        for (int i = 0; i < lanes; ++i) mx = fmaxf(mx, sm.red[i][h]);
-        const float ref = mx == -INFINITY ? 0.0f : mx;
-        __syncthreads();
-        float l = 0.0f;
-        for (int p = tid >> 4; p < n; p += lanes) {
-            const float2 ml = __ldcg(&A.part_ml[(static_cast<int64_t>(slot(p)) * A.tok_slots + tok) * kHeads + h]);
-            const float w = ga_ex2(ml.x - ref);
-            sm.w[p][h] = w;
-            l += ml.y * w;
-        }
-        sm.red[tid >> 4][h] = l;
-        __syncthreads();
-        const float wo = ga_ex2(own - ref);
-        l = wo;
-        for (int i = 0; i < lanes; ++i) l += sm.red[i][h];
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;             // a NaN stays one
-        if (col0 == 0 && tid < kHeads) A.lse[r] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
-        // 4 heads (hq) of one channel per thread, every fourth partial
-        const int grp = tid >> 6, col = (tid & 63) >> 2, hq = (tid & 3) * 4;
-        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int p = grp; p < n; p += 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                A.part_o + ((static_cast<int64_t>(slot(p)) * A.tok_slots + tok) * kDim + col0 + col) * kHeads + hq));
-            a.x += sm.w[p][hq] * v.x;
-            a.y += sm.w[p][hq + 1] * v.y;
-            a.z += sm.w[p][hq + 2] * v.z;
-            a.w += sm.w[p][hq + 3] * v.w;
-        }
-        sm.sum[grp][tid & 63] = a;
-        __syncthreads();
-        // one output per thread: head tid / 16, channel tid % 16
-        const int oh = tid >> 4, oc = tid & 15;
-        float v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v += reinterpret_cast<const float *>(&sm.sum[i][oc * 4 + (oh >> 2)])[oh & 3];
-        if (tid < kHeads) {
-            sm.red[0][h] = inv;
-            sm.fo[h] = wo > 0.0f ? wo * inv : 0.0f;                // nothing to read without an own part
-        }
-        __syncthreads();
-        const int64_t at = (static_cast<int64_t>(t.tok0 + tok) * kHeads + oh) * kDim + col0 + oc;
-        v *= sm.red[0][oh];
-        if (sm.fo[oh] != 0.0f) v += sm.fo[oh] * __ldg(A.o_own + at);
-        A.out[at] = __float2bfloat16_rn(v);
-        __syncthreads();
+        GmTile t;
+        t.c0 = lo - 1;
+        t.n = static_cast<int>(((tile.begin + tile.blocks) * ctas - 1) / total) - t.c0 + 1;
+        t.slot0 = 2 * t.c0 + (ga_range(total, t.c0, ctas) < tile.begin - kGaGap ? 1 : 0);   // a range's first tile: slot 0
+        const int64_t row = static_cast<int64_t>(tile.tok0 + tok) * kHeads;
+        gm_weights(A, sm, t, tok, row, slice == 0);
+        if (per == 36) gm_slice16(A, sm, t, tok, row, slice * 16);
+        else if (per == 9) gm_slice<1>(A, sm, t, tok, row, slice * 64);
+        else gm_slice<9>(A, sm, t, tok, row, 0);
     }
 }
 
