@@ -48,34 +48,29 @@
 namespace csa2 {
 
 constexpr int kGaMaxTokens = 1 << 20, kGaMaxGroups = 65535;
-constexpr int kGaMaxCtas = 160;
-constexpr int kGaTok = 8;                                          // tokens per row tile
-constexpr int kGaRows = kGaTok * kHeads;                           // 128
+constexpr int kGaMaxPairs = 80;
+constexpr int kGaTok = 16, kGaCtaTok = 8;                          // tokens per row tile; of each CTA of the pair
+constexpr int kGaRows = kGaCtaTok * kHeads;                        // 128
 constexpr int kGaBlk = kPage;                                      // keys per block
-constexpr int kGaSoftWarps = 8, kGaDeqWarps = 4;
-constexpr int kGaMmaWarp = kGaSoftWarps + kGaDeqWarps;
-constexpr int kGaThreads = (kGaMmaWarp + 4) * 32;                  // 512: whole warpgroups, for the register split
+constexpr int kGaSoftWarps = 8, kGaMmaWarp = 8, kGaKWarp = 9, kGaVWarp = 12, kGaCrew = 3;
+constexpr int kGaThreads = 16 * 32;                                // 512: whole warpgroups, for the register split
 // Registers per thread: 128 at launch (512 x 128 = the SM's 65,536); the two
-// softmax warpgroups take 160, the other two 96: (160 + 160 + 96 + 96) x 128
+// softmax warpgroups take 168, the other two 88: (168 + 168 + 88 + 88) x 128
 // threads = 65,536, the launch's own total.
-constexpr int kGaSoftRegs = 160, kGaOtherRegs = 96;
+constexpr int kGaSoftRegs = 168, kGaOtherRegs = 88;
 constexpr int kGaChunk = 64;                                       // channels per chunk
 constexpr int kGaChunks = kDim / kGaChunk;                         // 9
-constexpr int kGaQSlab = kGaRows * 16, kGaKSlab = kGaBlk * 16;     // 2,048 and 1,024 B: 8 channels of every row
-constexpr int kGaTmemCh = 416;                                     // channels accumulated in tensor memory
-constexpr int kGaSCol = kGaTmemCh, kGaPCol = kGaSCol + kGaBlk;     // 416, 480
-constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a softmax thread holds: 80
-// The chunks of a block in the order in which O's MMAs release them, so the
-// order in which they are refilled and multiplied for S; in groups with one
-// barrier each.
-constexpr int kGaGroups = 5;
-__device__ __forceinline__ constexpr int ga_order(int i) {          // 0 1 | 7 | 2 3 | 8 | 4 5 6
-    return i < 2 ? i : i == 2 ? 7 : i < 5 ? i - 1 : i == 5 ? 8 : i - 2;
-}
-__device__ __forceinline__ constexpr int ga_group_end(int g) { return g == 0 ? 2 : g == 1 ? 3 : g == 2 ? 5 : g == 3 ? 6 : 9; }
+constexpr int kGaCtaCh = kDim / 2;                                 // 288 channels of V per CTA
+constexpr int kGaQSlab = kGaRows * 16;                             // 2,048 B: 8 channels of every row
+constexpr int kGaKSlab = kGaBlk / 2 * 16, kGaVSlab = kGaBlk * 16;  // 512 and 1,024 B: of 32 keys, of 64 keys
+constexpr int kGaTmemCh = 384;                                     // channels accumulated in tensor memory
+constexpr int kGaSCol = kGaTmemCh, kGaDCol = kGaSCol + kGaBlk;     // 384, 448
+constexpr int kGaPCol = kGaDCol + 32;                              // 480
+constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a softmax thread holds: 96
+constexpr int kGaRounds = kGaChunks / kGaCrew;                     // chunks 3 i .. 3 i + 2 share barriers
 constexpr int kGaGap = 2;                                          // steps a row tile counts for beside its blocks
 constexpr float kGaSlack = 8.0f;                                   // log2 units a block may exceed the reference
-static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 80, "tensor memory is full; pieces of 64, 64 and 32 channels");
+static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 96, "tensor memory is full; pieces of 64, 32, 64 and 32 channels");
 
 struct GaArgs {
     const __nv_bfloat16 *q;            // [N][16][576]
@@ -91,20 +86,20 @@ struct GaArgs {
     __nv_bfloat16 *out;                // [N][16][576]
     float *lse;                        // [N][16]
     struct GaPlan *plan;
-    float *part_o;                     // [2 * CTAs][tok_slots][576][16]
-    float2 *part_ml;                   // [2 * CTAs][tok_slots * 16]: (m in the log2 domain, l)
-    int tok_slots;                     // min(8, N)
+    float *part_o;                     // [2 * ranges][tok_slots][576][16]
+    float2 *part_ml;                   // [2 * ranges][tok_slots * 16]: (m in the log2 domain, l)
+    int tok_slots;                     // min(16, N)
 };
 
 // What K13 has to know of K12's ranges.
 struct GaPlan {
     int64_t total;                     // steps of all row tiles
-    int ctas;                          // ranges
+    int ranges;
     // row tile of a range's first step; begin is the step of its first block
-    struct Tile { int64_t begin; int blocks, tok0, ntok; } first[kGaMaxCtas];
+    struct Tile { int64_t begin; int blocks, tok0, ntok; } first[kGaMaxPairs];
 };
 
-__host__ __device__ __forceinline__ int64_t ga_range(int64_t total, int c, int ctas) { return total * c / ctas; }
+__host__ __device__ __forceinline__ int64_t ga_range(int64_t total, int c, int ranges) { return total * c / ranges; }
 
 struct GaGroup { int tok0, n, T, blocks; };
 
@@ -138,7 +133,7 @@ __device__ __forceinline__ int64_t ga_steps(const GaGroup &g) {
     return static_cast<int64_t>((g.n + kGaTok - 1) / kGaTok) * (kGaGap + g.blocks);
 }
 
-// One row tile's blocks [k0, k1) of a CTA's range.
+// One row tile's blocks [k0, k1) of a pair's range.
 struct GaSeg {
     int g, tok0, ntok, T, blocks, k0, k1;
 };
@@ -174,11 +169,15 @@ struct GaWalk {
 
 struct GaSmem {
     alignas(1024) uint8_t q[kGaRows * kDim * 2];
-    alignas(1024) uint8_t k[kGaBlk * kDim * 2];
-    uint64_t q_full, s_full, p_full, d_full, d_empty, o_full;
-    uint64_t k_full[kGaGroups], k_free[kGaGroups];
+    alignas(1024) uint8_t k[kGaBlk / 2 * kDim * 2];                // this CTA's half of the block's keys
+    alignas(1024) uint8_t v[kGaBlk * kGaCtaCh * 2];                // this CTA's half of the channels
+    uint64_t q_full;                   // query tile in
+    uint64_t s_full, s_read;           // scores in tensor memory, in registers
+    uint64_t p_full;                   // probabilities in tensor memory
+    uint64_t ds_full, ds_empty;        // a piece in S's columns; read
+    uint64_t dd_full, dd_empty;        // a piece in its own 32 columns; read
+    uint64_t k_full[kGaRounds], k_free[kGaRounds], v_full[kGaRounds], v_free[kGaRounds];
     uint32_t tmem;
-    int valid[2];                      // keys of a block that count, by block parity
     float scale[kGaRows];              // a row's softmax scale (log2) times its query exponent
     float mx[2][2][kGaRows];           // a row's maximum in each half of a block, by block parity
     float l[kGaRows];
@@ -190,20 +189,58 @@ constexpr size_t kGaSmemBytes = sizeof(GaSmem);
 static_assert(kGaSmemBytes <= 232448, "one CTA per SM");
 
 // ---------------------------------------------------------------- PTX
-__device__ __forceinline__ void ga_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Barriers that the MMA thread waits for lie in the first CTA of the pair and
+// take arrivals of both; those that a commit completes lie in both. What an
+// arrival announces is read by the tensor cores only (shared memory after a
+// proxy fence, tensor memory after a tcgen05 fence), never by threads of the
+// other CTA, so it needs no cluster-wide release: with one, each arrival waits
+// for the warp's outstanding loads (2,000 cycles).
+__device__ __forceinline__ void ga_arrive_first(uint64_t *bar) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}"
+        ::"r"(smem_u32(bar)) : "memory");
+}
+
+// One arrival on the barrier at this place in both CTAs when the MMAs issued so far have completed.
+__device__ __forceinline__ void ga_commit(uint32_t one, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %2, 0;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+        ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)), "r"(one) : "memory");
+}
+
+__device__ __forceinline__ void ga_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The pair's MMAs, issued by the lane whose `one` is set; the warp stays
+// together, so that the operands are uniform. A descriptor is its low word
+// (address and leading offset) plus a constant under a constant high word.
+template <int kD, uint32_t kIdesc, uint32_t kA, uint32_t kAHi, uint32_t kB, uint32_t kBHi>
+__device__ __forceinline__ void ga_mma_ss(uint32_t one, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.u32 e, %9, 0;\n\tsetp.ne.u32 p, %2, 0;\n\tadd.u32 a, %0, %5;\n\tadd.u32 b, %1, %7;\n\t"
+        "mov.b64 da, {a, %6};\n\tmov.b64 db, {b, %8};\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%3], da, db, %4, p;\n\t}"
+        ::"r"(a_lo), "r"(b_lo), "r"(accumulate), "r"(kD), "n"(kIdesc), "n"(kA), "n"(kAHi), "n"(kB), "n"(kBHi), "r"(one)
+        : "memory");
 }
 
 // A from tensor memory: lane = row, a 32-bit column holds two f16 of the K side.
-__device__ __forceinline__ void ga_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+template <int kD, uint32_t kIdesc, int kACol, uint32_t kB, uint32_t kBHi>
+__device__ __forceinline__ void ga_mma_ts(uint32_t one, uint32_t b_lo, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+        "{\n\t.reg .pred e, p;\n\t.reg .b32 b;\n\t.reg .b64 db;\n\t"
+        "setp.ne.u32 e, %7, 0;\n\tsetp.ne.u32 p, %1, 0;\n\tadd.u32 b, %0, %5;\n\tmov.b64 db, {b, %6};\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%2], [%3], db, %4, p;\n\t}"
+        ::"r"(b_lo), "r"(accumulate), "r"(kD), "r"(kACol), "n"(kIdesc), "n"(kB), "n"(kBHi), "r"(one) : "memory");
 }
+
+// Words of a descriptor without swizzle (umma_desc).
+__device__ __forceinline__ uint32_t ga_desc_lo(const void *p, uint32_t lbo) { return (smem_u32(p) >> 4 & 0x3fffu) | lbo >> 4 << 16; }
+__device__ __forceinline__ constexpr uint32_t ga_desc_hi(uint32_t sbo) { return sbo >> 4 | 1u << 14; }
 
 __device__ __forceinline__ void ga_tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
@@ -249,16 +286,45 @@ __device__ __forceinline__ void ga_regs_down() { asm volatile("setmaxnreg.dec.sy
 
 __device__ __forceinline__ void ga_pair_bar(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 
-// A wait that a thread gives up for good after its first timeout.
+// A wait that a thread gives up for good after its first timeout. Its limit is
+// a number of probes of up to 1 us each (the sleeping probe's hint), 2 s in all:
+// the roles' loops press on the instruction cache, so it is kept short.
 struct GaWait {
     bool dead = false;
     __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
-        if (!dead) dead = !mbar_wait_bounded(bar, parity);
+        if (mbar_try_wait(bar, parity) || dead) return;
+        for (int i = 0; i < 2000000; ++i)
+            if (mbar_try_wait_sleep(bar, parity, 1000u)) return;
+        flag_status(kStatusTimeout);
+        dead = true;
     }
 };
 
+// Two waits whose probes (100 cycles each) overlap.
+__device__ __forceinline__ void ga_wait2(GaWait &wait, uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb) {
+    const bool oa = mbar_try_wait(a, pa), ob = mbar_try_wait(b, pb);
+    if (!oa) wait(a, pa);
+    if (!ob) wait(b, pb);
+}
+
+// Two floats at once.
+__device__ __forceinline__ float2 ga_fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 ga_add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // ---------------------------------------------------------------- roles
-// The first step of this CTA's range (its group, and that group's first step)
+// The first step of this pair's range (its group, and that group's first step)
 // and the total: a block scan over the groups, again over the chunks of 512
 // when there are more.
 __device__ __forceinline__ void ga_locate(const GaArgs &A, GaSmem &sm) {
@@ -286,8 +352,8 @@ __device__ __forceinline__ void ga_locate(const GaArgs &A, GaSmem &sm) {
     };
     for (int g0 = 0; g0 < A.G; g0 += kGaThreads) scan(g0, blockIdx.x == 0);
     const int64_t total = base;
-    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-    const int64_t want = static_cast<int>(blockIdx.x) < ctas ? ga_range(total, blockIdx.x, ctas) : -1;
+    const int ranges = static_cast<int>(min(static_cast<int64_t>(gridDim.x / 2), total)), range = blockIdx.x / 2;
+    const int64_t want = range < ranges ? ga_range(total, range, ranges) : -1;
     if (tid == 0) sm.total = total;
     base = 0;
     for (int g0 = 0; g0 < A.G; g0 += kGaThreads) {
@@ -304,14 +370,14 @@ __device__ __forceinline__ void ga_locate(const GaArgs &A, GaSmem &sm) {
 // matrices. The exponent is 0 as a rule, so the rows are stored as they come
 // and again only where the largest magnitude asks for another one. Kept small:
 // the code runs once per row tile, at the pace of the instruction fetch.
-__device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaSeg &s, int warp, int lane) {
-    const bool some = warp < s.ntok;
+__device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaSeg &s, int tok0, int warp, int lane) {
+    const bool some = tok0 + warp < s.ntok;                        // tok0: first token of this CTA in the row tile
     // a negative softmax scale turns the query round, so that the largest score has the largest logit
     const float sign = copysignf(1.0f, A.scale_log2);
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
         const int h = half * 8 + (lane & 7), row = warp * kHeads + h, part = lane >> 3;
-        const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (static_cast<int64_t>(s.tok0 + (some ? warp : 0)) * kHeads + h) * kDim) + part;
+        const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (static_cast<int64_t>(s.tok0 + (some ? tok0 + warp : 0)) * kHeads + h) * kDim) + part;
         uint8_t *dst = sm.q + part * kGaQSlab + row * 16;
         float mx = 0.0f, down = sign;
         for (int pass = 0; pass < 2; ++pass) {
@@ -335,7 +401,8 @@ __device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaS
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const int eq = f16_exponent(mx);
-            if (part == 0) sm.scale[row] = fabsf(A.scale_log2) * exp2f(static_cast<float>(eq));
+            // never 0: entries that do not count have a score of -inf, which has to stay one
+            if (part == 0) sm.scale[row] = fmaxf(fabsf(A.scale_log2) * exp2f(static_cast<float>(eq)), 1e-30f);
             if (!__any_sync(0xffffffffu, eq != 0)) break;
             down = sign * exp2f(static_cast<float>(-eq));
         }
@@ -343,11 +410,11 @@ __device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaS
 }
 
 // A segment of a group without entries: its tokens' own parts, or zeros.
-__device__ __forceinline__ void ga_own_only(const GaArgs &A, const GaSeg &s, int warp, int lane) {
-    if (warp >= s.ntok) return;
+__device__ __forceinline__ void ga_own_only(const GaArgs &A, const GaSeg &s, int tok, int lane) {
+    if (tok >= s.ntok) return;
 #pragma unroll 1
     for (int h = 0; h < kHeads; ++h) {
-        const int64_t r = static_cast<int64_t>(s.tok0 + warp) * kHeads + h;
+        const int64_t r = static_cast<int64_t>(s.tok0 + tok) * kHeads + h;
         const float own = A.lse_own ? __ldg(A.lse_own + r) : -INFINITY;
         if (lane == 0) A.lse[r] = own;
         for (int c = lane * 2; c < kDim; c += 64) {
@@ -358,120 +425,140 @@ __device__ __forceinline__ void ga_own_only(const GaArgs &A, const GaSeg &s, int
     }
 }
 
-// Channel of a softmax thread's output register i (a multiple of 16).
-__device__ __forceinline__ constexpr int ga_reg_channel(int i, int half) {
-    return i < 64 ? kGaTmemCh + (i & 32) * 2 + half * 32 + (i & 16) : kGaTmemCh + 128 + half * 16;
-}
+// An MMA of N columns of O takes N / 2 channels from each CTA's V, so column
+// 128 q + 64 half + i is channel 288 half + 64 q + i; the pieces hold channels
+// 288 half + 192 on, 32, 16, 32 and 16 of each half.
+__device__ __forceinline__ int ga_o_col(int c, int half) { return (c >> 6) * 128 + 64 * half + (c & 63); }
 
 __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk walk, int warp, int lane) {
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;      // keys 32 half ..; tile row
+    const int tok0 = (blockIdx.x & 1) * kGaCtaTok;                 // this CTA's tokens of a row tile
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;      // keys 32 half ..; row of the CTA
     const uint32_t tm = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int pair_bar = 1 + (warp & 3);                           // the two warps of the same rows
     GaWait wait;
-    uint32_t blk = 0, piece = 0, seg_no = 0, tile_no = 0;          // tile_no: segments with entries
+    uint32_t blk = 0, seg_no = 0;
     GaSeg s;
     while (walk.next(A, s)) {
         if (s.T == 0) {
-            ga_own_only(A, s, warp, lane);
+            ga_own_only(A, s, tok0 + warp, lane);
             ++seg_no;
             continue;
         }
-        ga_load_q(A, sm, s, warp, lane);
+        const int32_t *pages = A.page_table + static_cast<int64_t>(s.g) * A.max_pages;
+        int page = __ldg(pages + s.k0);
+        ga_load_q(A, sm, s, tok0, warp, lane);
         fence_proxy_async_smem();
         asm volatile("bar.sync 5, 256;" ::: "memory");             // scales of all rows; the tile is whole
-        if (threadIdx.x == 0) mbar_arrive(&sm.q_full);
+        if (threadIdx.x == 0) ga_arrive_first(&sm.q_full);
         const float scale = sm.scale[row];
         float m = -INFINITY, l = 0.0f;
-        float acc[kGaRegs];
+        float2 acc[kGaRegs / 2];
 #pragma unroll
-        for (int i = 0; i < kGaRegs; ++i) acc[i] = 0.0f;
-        for (int kb = s.k0; kb < s.k1; ++kb, ++blk) {
-            const uint32_t par = blk & 1u;
-            wait(&sm.s_full, par);
-            wait(&sm.k_full[kGaGroups - 1], par);                  // orders the read of valid[] as well
+        for (int i = 0; i < kGaRegs / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+        // adds this half's columns of a piece
+        auto piece_add = [&](auto n_, int to, uint64_t *full, uint64_t *empty, int col, uint32_t par) {
+            constexpr int kN = decltype(n_)::value;
+            wait(full, par);
             tc_fence_after();
-            float x[32];
-            ga_tmem_ld32(tm + kGaSCol + 32 * half, x);
-            const int n = sm.valid[par] - 32 * half;
-            if (n < 32) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = i < n ? x[i] : -INFINITY;
+            for (int c = 0; c < kN; c += 16) {
+                float a[16];
+                tmem_ld16(tm + col + kN * half + c, a);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    acc[(to + c) / 2 + i] = ga_add2(acc[(to + c) / 2 + i], make_float2(a[2 * i], a[2 * i + 1]));
             }
-            float mx = x[0];
-#pragma unroll
-            for (int i = 1; i < 32; ++i) mx = fmaxf(mx, x[i]);
-            sm.mx[par][half][row] = mx;
-            // with the reference as it stands; again below if the block's maximum moves it
-            float sum;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ga_arrive_first(empty);
+        };
+        // round kb: softmax of block kb, the pieces of block kb - 1, then block kb's probabilities
+        for (int kb = s.k0; kb <= s.k1; ++kb) {
+            const bool scores = kb < s.k1;
             uint32_t p[16];
-            auto exponentials = [&]() {
-                const float ref = m == -INFINITY ? 0.0f : m;
-                float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float sum = 0.0f, f = 1.0f;
+            bool any = false;
+            if (scores) {
+                const uint32_t par = blk & 1u;
+                ++blk;
+                const int n = (page >= 0 && page < A.num_pages ? min(kGaBlk, s.T - kb * kGaBlk) : 0) - 32 * half;
+                if (kb + 1 < s.k1) page = __ldg(pages + kb + 1);
+                wait(&sm.s_full, par);
+                tc_fence_after();
+                float x[32];
+                ga_tmem_ld32(tm + kGaSCol + 32 * half, x);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ga_arrive_first(&sm.s_read);
+                if (n < 32) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float a = ga_ex2(fmaf(x[2 * i], scale, -ref)), b = ga_ex2(fmaf(x[2 * i + 1], scale, -ref));
-                    if (n < 32) {                                  // -inf times a scale of 0
-                        a = 2 * i < n ? a : 0.0f;
-                        b = 2 * i + 1 < n ? b : 0.0f;
-                    }
-                    s4[i & 3] += a + b;
-                    p[i] = f32x2_f16x2(a, b);
+                    for (int i = 0; i < 32; ++i) x[i] = i < n ? x[i] : -INFINITY;
                 }
-                sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-            };
-            exponentials();
-            ga_pair_bar(pair_bar);
-            mx = fmaxf(mx, sm.mx[par][half ^ 1][row]);
-            mx = mx == -INFINITY ? mx : mx * scale;
-            const bool raise = mx > m + kGaSlack || (m == -INFINITY && mx > m);
-            if (__any_sync(0xffffffffu, raise)) {
-                const float f = raise ? ga_ex2(m - mx) : 1.0f;     // 0 for the first keys of a row
-                if (raise) m = mx;
+                float mx = fmaxf(x[0], x[1]);
+#pragma unroll
+                for (int i = 2; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[i], x[i + 1]));
+                sm.mx[par][half][row] = mx;
+                // with the reference as it stands; again if the block's maximum moves it
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+                    const float ref = m == -INFINITY ? 0.0f : -m;
+                    float2 s2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float2 e = ga_fma2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(scale, scale), make_float2(ref, ref));
+                        e.x = ga_ex2(e.x);
+                        e.y = ga_ex2(e.y);
+                        s2[i & 1] = ga_add2(s2[i & 1], e);
+                        p[i] = f32x2_f16x2(e.x, e.y);
+                    }
+                    s2[0] = ga_add2(s2[0], s2[1]);
+                    sum = s2[0].x + s2[0].y;
+                    if (pass == 1) break;
+                    ga_pair_bar(pair_bar);
+                    mx = fmaxf(mx, sm.mx[par][half ^ 1][row]);
+                    mx = mx == -INFINITY ? mx : mx * scale;
+                    const bool raise = mx > m + kGaSlack || (m == -INFINITY && mx > m);
+                    any = __any_sync(0xffffffffu, raise);
+                    if (!any) break;
+                    if (raise) {
+                        f = ga_ex2(m - mx);                        // 0 for the first keys of a row
+                        m = mx;
+                    }
+                }
+            }
+            if (kb > s.k0) {                                       // two pieces in each place
+                piece_add(std::integral_constant<int, 32>{}, 0, &sm.ds_full, &sm.ds_empty, kGaSCol, 0u);
+                piece_add(std::integral_constant<int, 16>{}, 32, &sm.dd_full, &sm.dd_empty, kGaDCol, 0u);
+                piece_add(std::integral_constant<int, 32>{}, 48, &sm.ds_full, &sm.ds_empty, kGaSCol, 1u);
+                piece_add(std::integral_constant<int, 16>{}, 80, &sm.dd_full, &sm.dd_empty, kGaDCol, 1u);
+            }
+            if (!scores) break;
+            // every MMA of the block before is done (its last piece has been read): O and P are this thread's
+            if (any) {
                 l *= f;
 #pragma unroll
-                for (int i = 0; i < kGaRegs; ++i) acc[i] *= f;
+                for (int i = 0; i < kGaRegs / 2; ++i) acc[i] = make_float2(acc[i].x * f, acc[i].y * f);
                 if (kb > s.k0) {
 #pragma unroll 1
                     for (int c = 0; c < kGaTmemCh / 2; c += 16) {
                         float a[16];
                         uint32_t o[16];
-                        const uint32_t at = tm + half * (kGaTmemCh / 2) + c;
+                        const uint32_t at = tm + ga_o_col(c, half);
                         tmem_ld16(at, a);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(a[i] * f);
                         ga_tmem_st16(at, o);
                     }
                 }
-                exponentials();
             }
             l += sum;
             ga_tmem_st16(tm + kGaPCol + 16 * half, p);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full);
-            // the block's pieces of 64, 64 and 32 channels: this half's columns
-            auto piece_add = [&](auto n_, int to) {
-                constexpr int kN = decltype(n_)::value;            // columns of this half
-                wait(&sm.d_full, piece & 1u);
-                ++piece;
-                tc_fence_after();
-                float a[kN];
-                if constexpr (kN == 32) ga_tmem_ld32(tm + kGaSCol + 32 * half, a);
-                else tmem_ld16(tm + kGaSCol + 16 * half, a);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.d_empty);
-#pragma unroll
-                for (int i = 0; i < kN; ++i) acc[to + i] += a[i];
-            };
-            piece_add(std::integral_constant<int, 32>{}, 0);
-            piece_add(std::integral_constant<int, 32>{}, 32);
-            piece_add(std::integral_constant<int, 16>{}, 64);
+            if (lane == 0) ga_arrive_first(&sm.p_full);
         }
         // ---- end of the segment
-        wait(&sm.o_full, tile_no & 1u);
-        tc_fence_after();
-        const int tok = row >> 4, h = row & 15;
+        const int tok = tok0 + (row >> 4), h = row & 15;
         const bool live = tok < s.ntok;
         if (half == 1) sm.l[row] = l;
         ga_pair_bar(pair_bar);
@@ -480,20 +567,23 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
         l = sm.l[row];
         if (s.k0 > 0 || s.k1 < s.blocks) {
             // part of a row tile: unnormalised
-            const int64_t slot = 2 * blockIdx.x + (seg_no > 0);
+            const int64_t slot = 2 * (blockIdx.x / 2) + (seg_no > 0);
             float *po = A.part_o + (slot * A.tok_slots + tok) * (kDim * kHeads) + h;
             if (live && half == 0) A.part_ml[(slot * A.tok_slots + tok) * kHeads + h] = make_float2(m, l);
 #pragma unroll 1
             for (int c = 0; c < kGaTmemCh / 2; c += 16) {
                 float a[16];
-                tmem_ld16(tm + half * (kGaTmemCh / 2) + c, a);
+                tmem_ld16(tm + ga_o_col(c, half), a);
                 if (live)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) po[(half * (kGaTmemCh / 2) + c + i) * kHeads] = a[i];
+                    for (int i = 0; i < 16; ++i) po[(kGaCtaCh * half + c + i) * kHeads] = a[i];
             }
             if (live)
 #pragma unroll
-                for (int i = 0; i < kGaRegs; ++i) po[(ga_reg_channel(i & ~15, half) + (i & 15)) * kHeads] = acc[i];
+                for (int i = 0; i < kGaRegs / 2; ++i) {
+                    po[(kGaCtaCh * half + kGaTmemCh / 2 + 2 * i) * kHeads] = acc[i].x;
+                    po[(kGaCtaCh * half + kGaTmemCh / 2 + 2 * i + 1) * kHeads] = acc[i].y;
+                }
         } else {
             // the whole row tile: join the token's own part and write it
             const int64_t r = static_cast<int64_t>(s.tok0 + (live ? tok : 0)) * kHeads + h;
@@ -533,191 +623,242 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
 #pragma unroll 1
             for (int c = 0; c < kGaTmemCh / 2; c += 16) {
                 float a[16];
-                tmem_ld16(tm + half * (kGaTmemCh / 2) + c, a);
-                if (live) write(half * (kGaTmemCh / 2) + c, a);
+                tmem_ld16(tm + ga_o_col(c, half), a);
+                if (live) write(kGaCtaCh * half + c, a);
             }
             if (live)
 #pragma unroll
-                for (int j = 0; j < kGaRegs; j += 16) write(ga_reg_channel(j, half), acc + j);
+                for (int j = 0; j < kGaRegs; j += 16) write(kGaCtaCh * half + kGaTmemCh / 2 + j, reinterpret_cast<const float *>(acc) + j);
         }
         tc_fence_before();
         ++seg_no;
-        ++tile_no;
     }
 }
 
-__device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk walk, int warp, int lane) {
-    const int key = warp * 16 + (lane & 15), part = lane >> 4;     // this thread's key and half of each chunk
+// Three warps of each CTA fill K and three V, each one chunk of every round: a
+// K chunk is 64 channels of this CTA's 32 keys, a V chunk 32 of
+// its channels for all 64 keys, either way two 16-byte loads per lane. The loads
+// of three chunks are in flight; one loop serves K and V, chunk by chunk (small
+// code, see GaWait). A warp passes every phase of the barriers it waits for, so
+// their parity is enough.
+struct GaRaw {
+    uint4 v[2];                        // 32 channels of two keys
+    uint32_t s[2];                     // their two scales each
+    int left;                          // keys that count from this lane's first on
+};
+
+__device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk walk, bool is_k, int place, int lane) {
+    const int rank = blockIdx.x & 1;
+    // first key and 16-byte piece of this lane; keys from its first to its second; pieces and bytes of a chunk
+    const int key = is_k ? 32 * rank + (lane & 15) : lane, piece = is_k ? lane >> 4 : 9 * rank;
+    const int step = is_k ? 16 : 32, pieces = is_k ? 2 : 1;
+    const uint32_t slab = is_k ? kGaKSlab : kGaVSlab, chunk = (is_k ? 8 : 4) * slab;
+    uint8_t *dst0 = is_k ? sm.k + 4 * (lane >> 4) * kGaKSlab + (lane & 15) * 16 : sm.v + lane * 16;
+    uint64_t *full = is_k ? sm.k_full : sm.v_full, *free_ = is_k ? sm.k_free : sm.v_free;
     GaWait wait;
-    uint4 raw[kGaChunks];                                          // 32 channels of each chunk: codes
-    uint32_t sc[kGaChunks];                                        // and their two E4M3 scales
-    const uint4 *codes = nullptr;
-    const uint16_t *scales = nullptr;
-    bool ok = false;                                               // the key counts; one that does not is zeros
+    // ---- the fetch cursor: place at of block kb of segment s
     GaSeg s = {};
-    int kb = 0, n = 0;
-    auto open = [&]() {                                            // block kb of segment s
-        n = min(kGaBlk, s.T - kb * kGaBlk);
-        int page = 0;
-        if (n > 0) {
-            page = __ldg(A.page_table + static_cast<int64_t>(s.g) * A.max_pages + kb);
-            if (page < 0 || page >= A.num_pages) {
-                flag_status(kStatusBounds);
-                n = 0;
-            }
-        }
-        n = max(n, 0);
-        ok = key < n;
-        const int64_t slot = static_cast<int64_t>(page) * kPage + key;
-        codes = reinterpret_cast<const uint4 *>(A.kv_fp4 + slot * kFp4Bytes) + part;
-        scales = reinterpret_cast<const uint16_t *>(A.kv_scale + slot * kScaleBytes) + part;
-    };
-    auto load = [&](int c) {
-        raw[c] = ok ? __ldg(codes + 2 * c) : make_uint4(0u, 0u, 0u, 0u);
-        sc[c] = ok ? __ldg(scales + 2 * c) : 0u;
-    };
-    auto advance = [&]() {                                         // the next segment with entries
+    int kb = 0, page = 0, left = 0, at = place;
+    const uint8_t *codes = nullptr, *scales = nullptr;
+    auto segment = [&]() {                                         // the next one with entries
         do {
             if (!walk.next(A, s)) return false;
         } while (s.T == 0);
+        kb = s.k0;
+        page = __ldg(A.page_table + static_cast<int64_t>(s.g) * A.max_pages + kb);
         return true;
     };
-    bool more = advance();
-    if (more) {
-        kb = s.k0;
-        open();
-#pragma unroll
-        for (int c = 0; c < kGaChunks; ++c) load(c);
-    }
-    for (uint32_t blk = 0; more; ++blk) {
-        if (warp == 0 && lane == 0) sm.valid[blk & 1u] = n;
-        if (++kb == s.k1) {                                        // the block after
-            more = advance();
-            kb = s.k0;
+    auto open = [&]() {                                            // block kb, whose page has been read
+        left = s.T - kb * kGaBlk - key;
+        if (page < 0 || page >= A.num_pages) {
+            flag_status(kStatusBounds);
+            left = 0;
+            page = 0;
         }
-        if (more) open();
+        const int64_t slot = static_cast<int64_t>(page) * kPage + key;
+        codes = A.kv_fp4 + slot * kFp4Bytes + 16 * piece;
+        scales = A.kv_scale + slot * kScaleBytes + 2 * piece;
+        if (kb + 1 < s.k1) page = __ldg(A.page_table + static_cast<int64_t>(s.g) * A.max_pages + kb + 1);
+    };
+    bool more = segment();
+    if (!more) return;
+    open();
+    auto fetch = [&](GaRaw &r) {
+        r.left = left;
+        const int off = at * pieces;
+        // unconditional, so that nothing waits for them here: the rows are in the page whether they count or not
 #pragma unroll
-        for (int g = 0; g < kGaGroups; ++g) {
-            if (blk > 0) wait(&sm.k_free[g], (blk - 1) & 1u);
+        for (int k = 0; k < 2; ++k) {
+            r.v[k] = __ldg(reinterpret_cast<const uint4 *>(codes + k * step * kFp4Bytes + 16 * off));
+            r.s[k] = __ldg(reinterpret_cast<const uint16_t *>(scales + k * step * kScaleBytes + 2 * off));
+        }
+        at += kGaCrew;
+        if (at >= kGaChunks) {                                     // the next block; at the end the last one again, unused
+            at = place;
+            if (++kb == s.k1) more = segment();
+            if (more) open();
+        }
+    };
+    GaRaw r0, r1, r2;
+    int todo = 0;                                                  // chunks fetched and not converted
+    fetch(r0);
+    fetch(r1);
+    fetch(r2);
+    todo = 3;
+    int round = 0;
+    uint32_t blk = 0;
+#pragma unroll 1
+    while (todo > 0) {
+        if (blk > 0) wait(&free_[round], (blk - 1) & 1u);
+        uint8_t *dst = dst0 + (round * kGaCrew + place) * chunk;
 #pragma unroll
-            for (int i = g == 0 ? 0 : ga_group_end(g - 1); i < ga_group_end(g); ++i) {
-                const int c = ga_order(i);
-                const uint32_t s2 = e4m3x2_to_f16x2(sc[c]);
-                const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t w = (&raw[c].x)[u], f = u < 2 ? sa : sb;
-                    *reinterpret_cast<uint4 *>(sm.k + (8 * c + 4 * part + u) * kGaKSlab + key * 16) =
-                        make_uint4(hmul2_u32(e2m1x2_to_f16x2(w & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2((w >> 8) & 0xffu), f),
-                                   hmul2_u32(e2m1x2_to_f16x2((w >> 16) & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2(w >> 24), f));
-                }
-                if (more) load(c);                                 // in flight until the next block's turn
+        for (int k = 0; k < 2; ++k) {
+            if (r0.left <= k * step) {                             // entries that do not count are zeros
+                r0.v[k] = make_uint4(0u, 0u, 0u, 0u);
+                r0.s[k] = 0u;
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.k_full[g]);
+            const uint32_t s2 = e4m3x2_to_f16x2(r0.s[k]);
+            const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const uint32_t w = (&r0.v[k].x)[v], f = v < 2 ? sa : sb;
+                *reinterpret_cast<uint4 *>(dst + v * slab + k * step * 16) = make_uint4(
+                    hmul2_u32(e2m1x2_to_f16x2(w & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2((w >> 8) & 0xffu), f),
+                    hmul2_u32(e2m1x2_to_f16x2((w >> 16) & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2(w >> 24), f));
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ga_arrive_first(&full[round]);
+        r0 = r1;
+        r1 = r2;
+        if (more) fetch(r2);
+        else --todo;
+        if (++round == kGaRounds) {
+            round = 0;
+            ++blk;
         }
     }
 }
 
-// The whole warp walks and waits; one elected thread issues. Offsets and shapes
-// are compile-time constants (run-time descriptors double an MMA's issue time)
-// and the tensor memory address is 0: all of it is allocated.
+// The tensor memory address is 0: all of it is allocated. The pair's MMAs take
+// 128 rows from each CTA and half of B's columns. K-major operands: leading
+// offset along K (8 channels), stride offset along the rows; MN-major (V):
+// along the keys, along the channels.
 template <int kN, int kCh, int kCol>
-__device__ __forceinline__ void ga_pv(uint64_t d_v, uint32_t accumulate) {
-    constexpr uint32_t id = umma_idesc(kGaRows, kN, false, true);
-#pragma unroll
-    for (int j = 0; j < kGaBlk / 16; ++j)
-        ga_mma_ts(kCol, kGaPCol + 8 * j, d_v + ((kCh / 8 * kGaKSlab + j * 256) >> 4), id, j > 0 ? 1u : accumulate);
+__device__ __forceinline__ void ga_pv(uint32_t one, uint32_t v_lo, uint32_t accumulate) {
+    constexpr uint32_t id = umma_idesc(2 * kGaRows, kN, false, true), at = kCh / 8 * kGaVSlab >> 4, hi = ga_desc_hi(kGaVSlab);
+    ga_mma_ts<kCol, id, kGaPCol, at, hi>(one, v_lo, accumulate);
+    ga_mma_ts<kCol, id, kGaPCol + 8, at + 16, hi>(one, v_lo, 1u);
+    ga_mma_ts<kCol, id, kGaPCol + 16, at + 32, hi>(one, v_lo, 1u);
+    ga_mma_ts<kCol, id, kGaPCol + 24, at + 48, hi>(one, v_lo, 1u);
 }
 
 __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk) {
-    // K-major: leading offset along K (8 channels), stride offset along the rows; MN-major: along the keys, along the channels
-    const uint64_t d_q = umma_desc(smem_u32(sm.q), kGaQSlab, 128, 0);
-    const uint64_t d_k = umma_desc(smem_u32(sm.k), kGaKSlab, 128, 0);
-    const uint64_t d_v = umma_desc(smem_u32(sm.k), 128, kGaKSlab, 0);
-    constexpr uint32_t id_qk = umma_idesc(kGaRows, kGaBlk, false, false);
+    const uint32_t one = ga_elect() ? 1u : 0u;
+    const uint32_t d_q = ga_desc_lo(sm.q, kGaQSlab), d_k = ga_desc_lo(sm.k, kGaKSlab), d_v = ga_desc_lo(sm.v, 128);
     GaWait wait;
-    uint32_t blk = 0, piece = 0, seg_no = 0;
+    uint32_t s_blk = 0, o_blk = 0, tile_no = 0;                    // S products, O products and tiles so far
     GaSeg s;
     while (walk.next(A, s)) {
         if (s.T == 0) continue;
-        wait(&sm.q_full, seg_no & 1u);
-        for (int kb = s.k0; kb < s.k1; ++kb, ++blk) {
-            const uint32_t par = blk & 1u, acc = kb > s.k0;
-            // S takes the columns of the pieces: the last one has been read
-            if (piece > 0) wait(&sm.d_empty, (piece - 1) & 1u);
-            tc_fence_after();
-#pragma unroll
-            for (int g = 0; g < kGaGroups; ++g) {
-                wait(&sm.k_full[g], par);
-                if (ga_elect()) {
-#pragma unroll
-                    for (int i = g == 0 ? 0 : ga_group_end(g - 1); i < ga_group_end(g); ++i)
-#pragma unroll
-                        for (int j = 0; j < kGaChunk / 16; ++j)
-                            ga_mma_ss(kGaSCol, d_q + ((ga_order(i) * 8 + j * 2) * kGaQSlab >> 4),
-                                      d_k + ((ga_order(i) * 8 + j * 2) * kGaKSlab >> 4), id_qk, i > 0 || j > 0);
-                    if (g == kGaGroups - 1) umma_commit(&sm.s_full);
+        wait(&sm.q_full, tile_no & 1u);
+        ++tile_no;
+        const int n = s.k1 - s.k0;
+        for (int t = 0; t <= n; ++t) {
+            const bool scores = t < n, output = t > 0;
+            const uint32_t acc = t > 1, kp = s_blk & 1u, vp = o_blk & 1u;
+            if (scores) {
+                // S's columns: the last piece there has been read (and the scores before it, see below)
+                if (o_blk > 0) ga_wait2(wait, &sm.ds_empty, 1u, &sm.k_full[0], kp);
+                else wait(&sm.k_full[0], kp);
+                constexpr uint32_t id = umma_idesc(2 * kGaRows, kGaBlk, false, false), hi = ga_desc_hi(128);
+                constexpr uint32_t da = 2 * kGaQSlab >> 4, db = 2 * kGaKSlab >> 4;      // 16 channels
+                uint32_t a = d_q, b = d_k;
+#pragma unroll 1
+                for (int i = 0; i < kGaRounds; ++i) {
+                    if (i > 0) wait(&sm.k_full[i], kp);
+                    tc_fence_after();
+                    ga_mma_ss<kGaSCol, id, 0, hi, 0, hi>(one, a, b, i > 0);
+                    ga_mma_ss<kGaSCol, id, da, hi, db, hi>(one, a, b, 1u);
+                    ga_mma_ss<kGaSCol, id, 2 * da, hi, 2 * db, hi>(one, a, b, 1u);
+                    ga_mma_ss<kGaSCol, id, 3 * da, hi, 3 * db, hi>(one, a, b, 1u);
+                    ga_mma_ss<kGaSCol, id, 4 * da, hi, 4 * db, hi>(one, a, b, 1u);
+                    ga_mma_ss<kGaSCol, id, 5 * da, hi, 5 * db, hi>(one, a, b, 1u);
+                    ga_mma_ss<kGaSCol, id, 6 * da, hi, 6 * db, hi>(one, a, b, 1u);
+                    ga_mma_ss<kGaSCol, id, 7 * da, hi, 7 * db, hi>(one, a, b, 1u);
+                    ga_mma_ss<kGaSCol, id, 8 * da, hi, 8 * db, hi>(one, a, b, 1u);
+                    ga_mma_ss<kGaSCol, id, 9 * da, hi, 9 * db, hi>(one, a, b, 1u);
+                    ga_mma_ss<kGaSCol, id, 10 * da, hi, 10 * db, hi>(one, a, b, 1u);
+                    ga_mma_ss<kGaSCol, id, 11 * da, hi, 11 * db, hi>(one, a, b, 1u);
+                    ga_commit(one, &sm.k_free[i]);
+                    a += 12 * da;
+                    b += 12 * db;
                 }
-                __syncwarp();
+                ga_commit(one, &sm.s_full);
+            } else if (o_blk > 0) {
+                wait(&sm.ds_empty, 1u);
             }
-            wait(&sm.p_full, par);
-            tc_fence_after();
-            // O in parts of 128, 128 and 160 channels between the pieces of 64, 64 and 32 (channels 416, 480 and
-            // 544 on), so that a piece is read while a part is multiplied
-            if (ga_elect()) {
-                ga_pv<64, 416, kGaSCol>(d_v, 0u);
-                umma_commit(&sm.d_full);
-                ga_pv<128, 0, 0>(d_v, acc);
-                umma_commit(&sm.k_free[0]);                        // chunks 0, 1
+            if (output) {
+                ga_wait2(wait, &sm.p_full, vp, &sm.v_full[0], vp);
+                tc_fence_after();
+                ga_pv<128, 0, 0>(one, d_v, acc);
+                wait(&sm.v_full[1], vp);
+                tc_fence_after();
+                ga_pv<128, 64, 128>(one, d_v, acc);
+                ga_commit(one, &sm.v_free[0]);
             }
-            __syncwarp();
-            wait(&sm.d_empty, piece & 1u);
-            tc_fence_after();
-            if (ga_elect()) {
-                ga_pv<64, 480, kGaSCol>(d_v, 0u);
-                umma_commit(&sm.d_full);
-                umma_commit(&sm.k_free[1]);                        // chunk 7
-                ga_pv<128, 128, 128>(d_v, acc);
-                umma_commit(&sm.k_free[2]);                        // chunks 2, 3
+            if (scores) {
+                wait(&sm.s_read, kp);                              // the scores are in registers: their columns are free
+                ++s_blk;
             }
-            __syncwarp();
-            wait(&sm.d_empty, (piece + 1) & 1u);
-            tc_fence_after();
-            if (ga_elect()) {
-                ga_pv<32, 544, kGaSCol>(d_v, 0u);
-                umma_commit(&sm.d_full);
-                umma_commit(&sm.k_free[3]);                        // chunk 8
-                ga_pv<160, 256, 256>(d_v, acc);
-                umma_commit(&sm.k_free[4]);                        // chunks 4, 5, 6
+            if (output) {
+                // the pieces, 64 columns of S's and 32 of their own, twice, each read while the next are multiplied
+                if (o_blk > 0) ga_wait2(wait, &sm.v_full[2], vp, &sm.dd_empty, 1u);
+                else wait(&sm.v_full[2], vp);
+                tc_fence_after();
+                ga_pv<64, 192, kGaSCol>(one, d_v, 0u);
+                ga_commit(one, &sm.ds_full);
+                ga_pv<32, 224, kGaDCol>(one, d_v, 0u);
+                ga_commit(one, &sm.dd_full);
+                ga_pv<128, 128, 256>(one, d_v, acc);
+                ga_commit(one, &sm.v_free[1]);
+                wait(&sm.ds_empty, 0u);
+                tc_fence_after();
+                ga_pv<64, 240, kGaSCol>(one, d_v, 0u);
+                ga_commit(one, &sm.ds_full);
+                wait(&sm.dd_empty, 0u);
+                tc_fence_after();
+                ga_pv<32, 272, kGaDCol>(one, d_v, 0u);
+                ga_commit(one, &sm.dd_full);
+                ga_commit(one, &sm.v_free[2]);
+                ++o_blk;
             }
-            __syncwarp();
-            piece += 3;
         }
-        if (ga_elect()) umma_commit(&sm.o_full);
-        __syncwarp();
-        ++seg_no;
     }
-    // every MMA of this CTA is done before tensor memory goes back
-    if (seg_no > 0) wait(&sm.o_full, (seg_no - 1) & 1u);
+    // every MMA of the pair is done before tensor memory goes back
+    if (o_blk > 0) wait(&sm.dd_full, 1u);
 }
 
-__global__ void __launch_bounds__(kGaThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGaThreads, 1)
 group_attn_kernel(const GaArgs A) {
     extern __shared__ __align__(1024) uint8_t ga_raw[];
     GaSmem &sm = *reinterpret_cast<GaSmem *>(ga_raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, range = blockIdx.x / 2;
     if (tid == 0) {
-        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_full, 2);
         mbar_init(&sm.s_full, 1);
-        mbar_init(&sm.p_full, kGaSoftWarps);
-        mbar_init(&sm.d_full, 1);
-        mbar_init(&sm.d_empty, kGaSoftWarps);
-        mbar_init(&sm.o_full, 1);
-        for (int c = 0; c < kGaGroups; ++c) {
-            mbar_init(&sm.k_full[c], kGaDeqWarps);
-            mbar_init(&sm.k_free[c], 1);
+        mbar_init(&sm.s_read, 2 * kGaSoftWarps);
+        mbar_init(&sm.p_full, 2 * kGaSoftWarps);
+        mbar_init(&sm.ds_full, 1);
+        mbar_init(&sm.ds_empty, 2 * kGaSoftWarps);
+        mbar_init(&sm.dd_full, 1);
+        mbar_init(&sm.dd_empty, 2 * kGaSoftWarps);
+        for (int i = 0; i < kGaRounds; ++i) {
+            mbar_init(&sm.k_full[i], 2 * kGaCrew);
+            mbar_init(&sm.v_full[i], 2 * kGaCrew);
+            mbar_init(&sm.k_free[i], 1);
+            mbar_init(&sm.v_free[i], 1);
         }
         fence_mbar_init();
     }
@@ -725,34 +866,37 @@ group_attn_kernel(const GaArgs A) {
     ga_locate(A, sm);
     __syncthreads();
     const int64_t total = sm.total;
-    const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    const int ranges = static_cast<int>(min(static_cast<int64_t>(gridDim.x / 2), total));
     if (blockIdx.x == 0 && tid == 0) {
         A.plan->total = total;
-        A.plan->ctas = ctas;
+        A.plan->ranges = ranges;
     }
-    if (static_cast<int>(blockIdx.x) >= ctas) return;
+    if (range >= ranges) return;                                   // both CTAs of the pair
     if (tid == 0) {
-        const int64_t at = ga_range(total, blockIdx.x, ctas), local = at - sm.start;
+        const int64_t at = ga_range(total, range, ranges), local = at - sm.start;
         const GaGroup grp = ga_group(A, sm.start_g, false);
         const int len = kGaGap + grp.blocks;
         GaWalk w;
-        w.left = ga_range(total, blockIdx.x + 1, ctas) - at;
+        w.left = ga_range(total, range + 1, ranges) - at;
         w.g = sm.start_g;
         w.tile = static_cast<int>(local / len);
         w.k = static_cast<int>(local - static_cast<int64_t>(w.tile) * len);
         sm.walk = w;
-        GaPlan::Tile &t = A.plan->first[blockIdx.x];
-        t.begin = at - w.k + kGaGap;
-        t.blocks = grp.blocks;
-        t.tok0 = grp.tok0 + w.tile * kGaTok;
-        t.ntok = min(kGaTok, grp.n - w.tile * kGaTok);
+        if ((blockIdx.x & 1) == 0) {
+            GaPlan::Tile &t = A.plan->first[range];
+            t.begin = at - w.k + kGaGap;
+            t.blocks = grp.blocks;
+            t.tok0 = grp.tok0 + w.tile * kGaTok;
+            t.ntok = min(kGaTok, grp.n - w.tile * kGaTok);
+        }
     }
     if (warp == kGaMmaWarp) {
-        tmem_alloc(&sm.tmem, 512);
-        tmem_relinquish();
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         tc_fence_before();
     }
     __syncthreads();
+    ga_cluster_sync();                                             // barriers and tensor memory of both CTAs
     tc_fence_after();
     const GaWalk walk = sm.walk;
     if (warp < kGaSoftWarps) {
@@ -760,18 +904,20 @@ group_attn_kernel(const GaArgs A) {
         ga_softmax(A, sm, walk, warp, lane);
     } else {
         ga_regs_down<kGaOtherRegs>();
-        if (warp < kGaMmaWarp)
-            ga_dequant(A, sm, walk, warp - kGaSoftWarps, lane);
-        else if (warp == kGaMmaWarp)
-            ga_mma(A, sm, walk);
+        if (warp == kGaMmaWarp) {
+            if ((blockIdx.x & 1) == 0) ga_mma(A, sm, walk);
+        } else if (warp < kGaVWarp + kGaCrew) {
+            ga_dequant(A, sm, walk, warp < kGaVWarp, (warp - kGaKWarp) % kGaCrew, lane);
+        }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    ga_cluster_sync();                                             // no arrival is on its way to a CTA that has ended
     pdl_trigger();
     if (warp == kGaMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(sm.tmem, 512);
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
     }
 }
 
@@ -785,14 +931,14 @@ group_attn_kernel(const GaArgs A) {
 constexpr int kGmThreads = 256;
 
 struct GmSmem {
-    float w[kGaMaxCtas + 1][kHeads];                               // weight of a partial
+    float w[kGaMaxPairs + 1][kHeads];                               // weight of a partial
     float red[kGmThreads / kHeads][kHeads];
     union {
         float4 sum[4][64];
         alignas(16) uint16_t out[kHeads][kDim + 8];
     };
     float inv[kHeads], fo[kHeads];
-    int first[kGaMaxCtas + 1];                                     // units before the c-th boundary's tile
+    int first[kGaMaxPairs + 1];                                     // units before the c-th boundary's tile
     int warp_sum[kGmThreads / 32];
 };
 
@@ -804,7 +950,7 @@ struct GmTile {
 
 __device__ __forceinline__ void gm_weights(const GaArgs &A, GmSmem &sm, const GmTile &t, int tok, int64_t row, bool first) {
     const int tid = threadIdx.x, h = tid & (kHeads - 1), at = tid >> 4;
-    constexpr int kLanes = kGmThreads / kHeads, kMost = (kGaMaxCtas + kLanes) / kLanes;
+    constexpr int kLanes = kGmThreads / kHeads, kMost = (kGaMaxPairs + kLanes) / kLanes;
     float2 ml[kMost];
     float own = -INFINITY;
     if (A.lse_own) own = __ldg(A.lse_own + row + h) * 1.4426950408889634f;
@@ -919,13 +1065,13 @@ group_attn_merge_kernel(const GaArgs A) {
     pdl_wait();
     pdl_trigger();
     const int64_t total = A.plan->total;
-    const int ctas = A.plan->ctas;
+    const int ranges = A.plan->ranges;
     // The range boundary c cuts the row tile of range c's first step when the
     // tile begins before it; the first such boundary of a tile stands for it.
     int mine = 0;
-    if (tid > 0 && tid < ctas) {
+    if (tid > 0 && tid < ranges) {
         const GaPlan::Tile &t = A.plan->first[tid];
-        if (t.begin < ga_range(total, tid, ctas) && t.begin >= ga_range(total, tid - 1, ctas)) mine = t.ntok;
+        if (t.begin < ga_range(total, tid, ranges) && t.begin >= ga_range(total, tid - 1, ranges)) mine = t.ntok;
     }
     int incl = mine;
 #pragma unroll
@@ -936,27 +1082,27 @@ group_attn_merge_kernel(const GaArgs A) {
     if (lane == 31) sm.warp_sum[warp] = incl;
     __syncthreads();
     for (int w = 0; w < warp; ++w) incl += sm.warp_sum[w];
-    if (tid < kGaMaxCtas) sm.first[tid + 1] = incl;                // tokens up to boundary tid
+    if (tid < kGaMaxPairs) sm.first[tid + 1] = incl;                // tokens up to boundary tid
     if (tid == 0) sm.first[0] = 0;
     __syncthreads();
-    const int tokens = sm.first[kGaMaxCtas];
+    const int tokens = sm.first[kGaMaxPairs];
     // slices of 16 channels while 36 of them per token fit one wave of CTAs, then of 64, then whole tokens
     const int grid = static_cast<int>(gridDim.x);
     const int per = tokens * 36 <= grid ? 36 : tokens * 9 <= 2 * grid ? 9 : 1;
     for (int unit = blockIdx.x; unit < tokens * per; unit += grid) {
         const int ut = unit / per, slice = unit - ut * per;
-        int lo = 0, hi = kGaMaxCtas;                               // the boundary: first[c] <= ut < first[c + 1]
+        int lo = 0, hi = kGaMaxPairs;                               // the boundary: first[c] <= ut < first[c + 1]
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (sm.first[mid] <= ut) lo = mid; else hi = mid;
         }
         const GaPlan::Tile tile = A.plan->first[lo];
         const int tok = ut - sm.first[lo];
-        // ranges lo - 1 (which begins the tile) to the last c with total * c / ctas < the tile's end
+        // ranges lo - 1 (which begins the tile) to the last c with total * c / ranges < the tile's end
         GmTile t;
         t.c0 = lo - 1;
-        t.n = static_cast<int>(((tile.begin + tile.blocks) * ctas - 1) / total) - t.c0 + 1;
-        t.slot0 = 2 * t.c0 + (ga_range(total, t.c0, ctas) < tile.begin - kGaGap ? 1 : 0);   // a range's first tile: slot 0
+        t.n = static_cast<int>(((tile.begin + tile.blocks) * ranges - 1) / total) - t.c0 + 1;
+        t.slot0 = 2 * t.c0 + (ga_range(total, t.c0, ranges) < tile.begin - kGaGap ? 1 : 0);   // a range's first tile: slot 0
         const int64_t row = static_cast<int64_t>(tile.tok0 + tok) * kHeads;
         gm_weights(A, sm, t, tok, row, slice == 0);
         if (per == 36) gm_slice16(A, sm, t, tok, row, slice * 16);
@@ -965,11 +1111,11 @@ group_attn_merge_kernel(const GaArgs A) {
     }
 }
 
-// Workspace: the plan, then two partials per CTA.
+// Workspace: the plan, then two partials per range.
 inline size_t ga_plan_bytes() { return (sizeof(GaPlan) + 255) / 256 * 256; }
-inline size_t ga_ml_bytes(int tok_slots) { return static_cast<size_t>(2 * kGaMaxCtas) * tok_slots * kHeads * sizeof(float2); }
+inline size_t ga_ml_bytes(int tok_slots) { return static_cast<size_t>(2 * kGaMaxPairs) * tok_slots * kHeads * sizeof(float2); }
 inline size_t ga_ws_bytes(int tok_slots) {
-    return ga_plan_bytes() + ga_ml_bytes(tok_slots) + static_cast<size_t>(2 * kGaMaxCtas) * tok_slots * kHeads * kDim * 4;
+    return ga_plan_bytes() + ga_ml_bytes(tok_slots) + static_cast<size_t>(2 * kGaMaxPairs) * tok_slots * kHeads * kDim * 4;
 }
 
 }  // namespace csa2
