@@ -696,7 +696,7 @@ csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D, const csa2_
     A.part_ml = reinterpret_cast<float2 *>(base + ga_plan_bytes());
     A.part_o = reinterpret_cast<float *>(base + ga_plan_bytes() + ga_ml_bytes(A.tok_slots));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int ctas = 2 * std::min(dev->sm_count / 2, kGaMaxPairs);
+    const int ctas = std::min(dev->sm_count, kGaMaxCtas);
     cudaError_t e = launch_pdl(group_attn_kernel, dim3(ctas), dim3(kGaThreads), kGaSmemBytes, st, A);
     if (e != cudaSuccess) return CSA2_ERR_CUDA;
     return cuda_status(launch_pdl(group_attn_merge_kernel, dim3(4 * ctas), dim3(kGmThreads), 0, st, A));

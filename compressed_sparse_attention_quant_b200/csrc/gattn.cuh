@@ -48,29 +48,28 @@
 namespace csa2 {
 
 constexpr int kGaMaxTokens = 1 << 20, kGaMaxGroups = 65535;
-constexpr int kGaMaxPairs = 80;
-constexpr int kGaTok = 16, kGaCtaTok = 8;                          // tokens per row tile; of each CTA of the pair
-constexpr int kGaRows = kGaCtaTok * kHeads;                        // 128
+constexpr int kGaMaxCtas = 160;
+constexpr int kGaTok = 8;                                          // tokens per row tile
+constexpr int kGaRows = kGaTok * kHeads;                           // 128
 constexpr int kGaBlk = kPage;                                      // keys per block
-constexpr int kGaSoftWarps = 8, kGaMmaWarp = 8, kGaKWarp = 9, kGaVWarp = 12, kGaCrew = 3;
+constexpr int kGaSoftWarps = 8, kGaMmaWarp = 8, kGaDeqWarp = 9, kGaDeqWarps = 6;
 constexpr int kGaThreads = 16 * 32;                                // 512: whole warpgroups, for the register split
 // Registers per thread: 128 at launch (512 x 128 = the SM's 65,536); the two
 // softmax warpgroups take 168, the other two 88: (168 + 168 + 88 + 88) x 128
 // threads = 65,536, the launch's own total.
 constexpr int kGaSoftRegs = 168, kGaOtherRegs = 88;
 constexpr int kGaChunk = 64;                                       // channels per chunk
-constexpr int kGaChunks = kDim / kGaChunk;                         // 9
-constexpr int kGaCtaCh = kDim / 2;                                 // 288 channels of V per CTA
-constexpr int kGaQSlab = kGaRows * 16;                             // 2,048 B: 8 channels of every row
-constexpr int kGaKSlab = kGaBlk / 2 * 16, kGaVSlab = kGaBlk * 16;  // 512 and 1,024 B: of 32 keys, of 64 keys
-constexpr int kGaTmemCh = 384;                                     // channels accumulated in tensor memory
-constexpr int kGaSCol = kGaTmemCh, kGaDCol = kGaSCol + kGaBlk;     // 384, 448
-constexpr int kGaPCol = kGaDCol + 32;                              // 480
-constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a softmax thread holds: 96
-constexpr int kGaRounds = kGaChunks / kGaCrew;                     // chunks 3 i .. 3 i + 2 share barriers
+constexpr int kGaQSlab = kGaRows * 16, kGaKSlab = kGaBlk * 16;     // 2,048 and 1,024 B: 8 channels of every row
+constexpr int kGaTmemCh = 416;                                     // channels accumulated in tensor memory
+constexpr int kGaSCol = kGaTmemCh, kGaPCol = kGaSCol + kGaBlk;     // 416, 480
+constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a softmax thread holds: 80
+// A block's nine chunks are filled, multiplied and released in three rounds, in
+// the order in which O's MMAs are done with them: 0 1 7, 2 3 8, 4 5 6.
+constexpr int kGaRounds = 3;
+__device__ __forceinline__ int ga_third_chunk(int round) { return round == 2 ? 6 : 7 + round; }
 constexpr int kGaGap = 2;                                          // steps a row tile counts for beside its blocks
 constexpr float kGaSlack = 8.0f;                                   // log2 units a block may exceed the reference
-static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 96, "tensor memory is full; pieces of 64, 32, 64 and 32 channels");
+static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 80, "tensor memory is full; pieces of 64, 64 and 32 channels");
 
 struct GaArgs {
     const __nv_bfloat16 *q;            // [N][16][576]
@@ -88,7 +87,7 @@ struct GaArgs {
     struct GaPlan *plan;
     float *part_o;                     // [2 * ranges][tok_slots][576][16]
     float2 *part_ml;                   // [2 * ranges][tok_slots * 16]: (m in the log2 domain, l)
-    int tok_slots;                     // min(16, N)
+    int tok_slots;                     // min(8, N)
 };
 
 // What K13 has to know of K12's ranges.
@@ -96,7 +95,7 @@ struct GaPlan {
     int64_t total;                     // steps of all row tiles
     int ranges;
     // row tile of a range's first step; begin is the step of its first block
-    struct Tile { int64_t begin; int blocks, tok0, ntok; } first[kGaMaxPairs];
+    struct Tile { int64_t begin; int blocks, tok0, ntok; } first[kGaMaxCtas];
 };
 
 __host__ __device__ __forceinline__ int64_t ga_range(int64_t total, int c, int ranges) { return total * c / ranges; }
@@ -133,7 +132,7 @@ __device__ __forceinline__ int64_t ga_steps(const GaGroup &g) {
     return static_cast<int64_t>((g.n + kGaTok - 1) / kGaTok) * (kGaGap + g.blocks);
 }
 
-// One row tile's blocks [k0, k1) of a pair's range.
+// One row tile's blocks [k0, k1) of a CTA's range.
 struct GaSeg {
     int g, tok0, ntok, T, blocks, k0, k1;
 };
@@ -169,14 +168,13 @@ struct GaWalk {
 
 struct GaSmem {
     alignas(1024) uint8_t q[kGaRows * kDim * 2];
-    alignas(1024) uint8_t k[kGaBlk / 2 * kDim * 2];                // this CTA's half of the block's keys
-    alignas(1024) uint8_t v[kGaBlk * kGaCtaCh * 2];                // this CTA's half of the channels
+    alignas(1024) uint8_t k[kGaBlk * kDim * 2];
     uint64_t q_full;                   // query tile in
-    uint64_t s_full, s_read;           // scores in tensor memory, in registers
-    uint64_t p_full;                   // probabilities in tensor memory
-    uint64_t ds_full, ds_empty;        // a piece in S's columns; read
-    uint64_t dd_full, dd_empty;        // a piece in its own 32 columns; read
-    uint64_t k_full[kGaRounds], k_free[kGaRounds], v_full[kGaRounds], v_free[kGaRounds];
+    uint64_t s_full;                   // scores in tensor memory
+    uint64_t p_full;                   // probabilities in tensor memory, O rescaled
+    uint64_t d_full, d_empty;          // a piece in S's columns; read
+    uint64_t o_done;                   // a block's O is complete
+    uint64_t k_full[kGaRounds], k_free[kGaRounds];
     uint32_t tmem;
     float scale[kGaRows];              // a row's softmax scale (log2) times its query exponent
     float mx[2][2][kGaRows];           // a row's maximum in each half of a block, by block parity
@@ -189,32 +187,15 @@ constexpr size_t kGaSmemBytes = sizeof(GaSmem);
 static_assert(kGaSmemBytes <= 232448, "one CTA per SM");
 
 // ---------------------------------------------------------------- PTX
-// Barriers that the MMA thread waits for lie in the first CTA of the pair and
-// take arrivals of both; those that a commit completes lie in both. What an
-// arrival announces is read by the tensor cores only (shared memory after a
-// proxy fence, tensor memory after a tcgen05 fence), never by threads of the
-// other CTA, so it needs no cluster-wide release: with one, each arrival waits
-// for the warp's outstanding loads (2,000 cycles).
-__device__ __forceinline__ void ga_arrive_first(uint64_t *bar) {
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}"
-        ::"r"(smem_u32(bar)) : "memory");
-}
-
-// One arrival on the barrier at this place in both CTAs when the MMAs issued so far have completed.
+// One arrival when the MMAs issued so far by this lane have completed.
 __device__ __forceinline__ void ga_commit(uint32_t one, uint64_t *bar) {
     asm volatile(
-        "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %2, 0;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
-        ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)), "r"(one) : "memory");
+        "{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(smem_u32(bar)), "r"(one) : "memory");
 }
 
-__device__ __forceinline__ void ga_cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The pair's MMAs, issued by the lane whose `one` is set; the warp stays
+// MMAs are issued by the lane whose `one` is set; the warp stays
 // together, so that the operands are uniform. A descriptor is its low word
 // (address and leading offset) plus a constant under a constant high word.
 template <int kD, uint32_t kIdesc, uint32_t kA, uint32_t kAHi, uint32_t kB, uint32_t kBHi>
@@ -223,7 +204,7 @@ __device__ __forceinline__ void ga_mma_ss(uint32_t one, uint32_t a_lo, uint32_t 
         "{\n\t.reg .pred e, p;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\t"
         "setp.ne.u32 e, %9, 0;\n\tsetp.ne.u32 p, %2, 0;\n\tadd.u32 a, %0, %5;\n\tadd.u32 b, %1, %7;\n\t"
         "mov.b64 da, {a, %6};\n\tmov.b64 db, {b, %8};\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%3], da, db, %4, p;\n\t}"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%3], da, db, %4, p;\n\t}"
         ::"r"(a_lo), "r"(b_lo), "r"(accumulate), "r"(kD), "n"(kIdesc), "n"(kA), "n"(kAHi), "n"(kB), "n"(kBHi), "r"(one)
         : "memory");
 }
@@ -234,7 +215,7 @@ __device__ __forceinline__ void ga_mma_ts(uint32_t one, uint32_t b_lo, uint32_t 
     asm volatile(
         "{\n\t.reg .pred e, p;\n\t.reg .b32 b;\n\t.reg .b64 db;\n\t"
         "setp.ne.u32 e, %7, 0;\n\tsetp.ne.u32 p, %1, 0;\n\tadd.u32 b, %0, %5;\n\tmov.b64 db, {b, %6};\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%2], [%3], db, %4, p;\n\t}"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%2], [%3], db, %4, p;\n\t}"
         ::"r"(b_lo), "r"(accumulate), "r"(kD), "r"(kACol), "n"(kIdesc), "n"(kB), "n"(kBHi), "r"(one) : "memory");
 }
 
@@ -324,7 +305,7 @@ __device__ __forceinline__ float2 ga_add2(float2 a, float2 b) {
 }
 
 // ---------------------------------------------------------------- roles
-// The first step of this pair's range (its group, and that group's first step)
+// The first step of this CTA's range (its group, and that group's first step)
 // and the total: a block scan over the groups, again over the chunks of 512
 // when there are more.
 __device__ __forceinline__ void ga_locate(const GaArgs &A, GaSmem &sm) {
@@ -352,7 +333,7 @@ __device__ __forceinline__ void ga_locate(const GaArgs &A, GaSmem &sm) {
     };
     for (int g0 = 0; g0 < A.G; g0 += kGaThreads) scan(g0, blockIdx.x == 0);
     const int64_t total = base;
-    const int ranges = static_cast<int>(min(static_cast<int64_t>(gridDim.x / 2), total)), range = blockIdx.x / 2;
+    const int ranges = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total)), range = blockIdx.x;
     const int64_t want = range < ranges ? ga_range(total, range, ranges) : -1;
     if (tid == 0) sm.total = total;
     base = 0;
@@ -370,14 +351,14 @@ __device__ __forceinline__ void ga_locate(const GaArgs &A, GaSmem &sm) {
 // matrices. The exponent is 0 as a rule, so the rows are stored as they come
 // and again only where the largest magnitude asks for another one. Kept small:
 // the code runs once per row tile, at the pace of the instruction fetch.
-__device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaSeg &s, int tok0, int warp, int lane) {
-    const bool some = tok0 + warp < s.ntok;                        // tok0: first token of this CTA in the row tile
+__device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaSeg &s, int warp, int lane) {
+    const bool some = warp < s.ntok;
     // a negative softmax scale turns the query round, so that the largest score has the largest logit
     const float sign = copysignf(1.0f, A.scale_log2);
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
         const int h = half * 8 + (lane & 7), row = warp * kHeads + h, part = lane >> 3;
-        const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (static_cast<int64_t>(s.tok0 + (some ? tok0 + warp : 0)) * kHeads + h) * kDim) + part;
+        const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (static_cast<int64_t>(s.tok0 + (some ? warp : 0)) * kHeads + h) * kDim) + part;
         uint8_t *dst = sm.q + part * kGaQSlab + row * 16;
         float mx = 0.0f, down = sign;
         for (int pass = 0; pass < 2; ++pass) {
@@ -425,125 +406,132 @@ __device__ __forceinline__ void ga_own_only(const GaArgs &A, const GaSeg &s, int
     }
 }
 
-// An MMA of N columns of O takes N / 2 channels from each CTA's V, so column
-// 128 q + 64 half + i is channel 288 half + 64 q + i; the pieces hold channels
-// 288 half + 192 on, 32, 16, 32 and 16 of each half.
-__device__ __forceinline__ int ga_o_col(int c, int half) { return (c >> 6) * 128 + 64 * half + (c & 63); }
+// Channel of a softmax thread's output register i (a multiple of 16): pieces
+// of 64, 64 and 32 channels, half of each.
+__device__ __forceinline__ constexpr int ga_reg_channel(int i, int half) {
+    return i < 64 ? kGaTmemCh + (i & 32) * 2 + half * 32 + (i & 16) : kGaTmemCh + 128 + half * 16;
+}
+
+// 16 channels of a row's result from ch on: the entries' sums times fk, the own part times fo.
+__device__ __forceinline__ void ga_write16(const GaArgs &A, int64_t row, int ch, const float *a, float fk, float fo) {
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = a[i] * fk;
+    if (fo != 0.0f) {
+        const float4 *own = reinterpret_cast<const float4 *>(A.o_own + row * kDim + ch);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 o = __ldg(own + i);
+            v[4 * i] += fo * o.x;
+            v[4 * i + 1] += fo * o.y;
+            v[4 * i + 2] += fo * o.z;
+            v[4 * i + 3] += fo * o.w;
+        }
+    }
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        b[i] = *reinterpret_cast<const uint32_t *>(&t);
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(A.out + row * kDim + ch);
+    dst[0] = make_uint4(b[0], b[1], b[2], b[3]);
+    dst[1] = make_uint4(b[4], b[5], b[6], b[7]);
+}
 
 __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk walk, int warp, int lane) {
-    const int tok0 = (blockIdx.x & 1) * kGaCtaTok;                 // this CTA's tokens of a row tile
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;      // keys 32 half ..; row of the CTA
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;      // keys 32 half ..; tile row
     const uint32_t tm = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int pair_bar = 1 + (warp & 3);                           // the two warps of the same rows
     GaWait wait;
-    uint32_t blk = 0, seg_no = 0;
+    uint32_t blk = 0, piece = 0, seg_no = 0;
     GaSeg s;
     while (walk.next(A, s)) {
         if (s.T == 0) {
-            ga_own_only(A, s, tok0 + warp, lane);
+            ga_own_only(A, s, warp, lane);
             ++seg_no;
             continue;
         }
         const int32_t *pages = A.page_table + static_cast<int64_t>(s.g) * A.max_pages;
         int page = __ldg(pages + s.k0);
-        ga_load_q(A, sm, s, tok0, warp, lane);
+        ga_load_q(A, sm, s, warp, lane);
         fence_proxy_async_smem();
         asm volatile("bar.sync 5, 256;" ::: "memory");             // scales of all rows; the tile is whole
-        if (threadIdx.x == 0) ga_arrive_first(&sm.q_full);
+        if (threadIdx.x == 0) mbar_arrive(&sm.q_full);
         const float scale = sm.scale[row];
         float m = -INFINITY, l = 0.0f;
         float2 acc[kGaRegs / 2];
 #pragma unroll
         for (int i = 0; i < kGaRegs / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
         // adds this half's columns of a piece
-        auto piece_add = [&](auto n_, int to, uint64_t *full, uint64_t *empty, int col, uint32_t par) {
+        auto piece_add = [&](auto n_, int to) {
             constexpr int kN = decltype(n_)::value;
-            wait(full, par);
+            wait(&sm.d_full, piece & 1u);
+            ++piece;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < kN; c += 16) {
                 float a[16];
-                tmem_ld16(tm + col + kN * half + c, a);
+                tmem_ld16(tm + kGaSCol + kN * half + c, a);
+                if (c + 16 == kN) {                                // the columns are free
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.d_empty);
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     acc[(to + c) / 2 + i] = ga_add2(acc[(to + c) / 2 + i], make_float2(a[2 * i], a[2 * i + 1]));
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ga_arrive_first(empty);
         };
-        // round kb: softmax of block kb, the pieces of block kb - 1, then block kb's probabilities
-        for (int kb = s.k0; kb <= s.k1; ++kb) {
-            const bool scores = kb < s.k1;
+        for (int kb = s.k0; kb < s.k1; ++kb, ++blk) {
+            const uint32_t par = blk & 1u;
+            const int n = (page >= 0 && page < A.num_pages ? min(kGaBlk, s.T - kb * kGaBlk) : 0) - 32 * half;
+            if (kb + 1 < s.k1) page = __ldg(pages + kb + 1);
+            wait(&sm.s_full, par);
+            tc_fence_after();
+            float x[32];
+            ga_tmem_ld32(tm + kGaSCol + 32 * half, x);
+            if (n < 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = i < n ? x[i] : -INFINITY;
+            }
+            float mx = fmaxf(x[0], x[1]);
+#pragma unroll
+            for (int i = 2; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[i], x[i + 1]));
+            sm.mx[par][half][row] = mx;
+            // with the reference as it stands; again if the block's maximum moves it
             uint32_t p[16];
-            float sum = 0.0f, f = 1.0f;
-            bool any = false;
-            if (scores) {
-                const uint32_t par = blk & 1u;
-                ++blk;
-                const int n = (page >= 0 && page < A.num_pages ? min(kGaBlk, s.T - kb * kGaBlk) : 0) - 32 * half;
-                if (kb + 1 < s.k1) page = __ldg(pages + kb + 1);
-                wait(&sm.s_full, par);
-                tc_fence_after();
-                float x[32];
-                ga_tmem_ld32(tm + kGaSCol + 32 * half, x);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ga_arrive_first(&sm.s_read);
-                if (n < 32) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = i < n ? x[i] : -INFINITY;
-                }
-                float mx = fmaxf(x[0], x[1]);
-#pragma unroll
-                for (int i = 2; i < 32; i += 2) mx = fmaxf(mx, fmaxf(x[i], x[i + 1]));
-                sm.mx[par][half][row] = mx;
-                // with the reference as it stands; again if the block's maximum moves it
+            float2 sum;
 #pragma unroll 1
-                for (int pass = 0; pass < 2; ++pass) {
-                    const float ref = m == -INFINITY ? 0.0f : -m;
-                    float2 s2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            for (int pass = 0; pass < 2; ++pass) {
+                const float ref = m == -INFINITY ? 0.0f : -m;
+                const float2 sc = make_float2(scale, scale), rf = make_float2(ref, ref);
+                sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float2 e = ga_fma2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(scale, scale), make_float2(ref, ref));
-                        e.x = ga_ex2(e.x);
-                        e.y = ga_ex2(e.y);
-                        s2[i & 1] = ga_add2(s2[i & 1], e);
-                        p[i] = f32x2_f16x2(e.x, e.y);
-                    }
-                    s2[0] = ga_add2(s2[0], s2[1]);
-                    sum = s2[0].x + s2[0].y;
-                    if (pass == 1) break;
-                    ga_pair_bar(pair_bar);
-                    mx = fmaxf(mx, sm.mx[par][half ^ 1][row]);
-                    mx = mx == -INFINITY ? mx : mx * scale;
-                    const bool raise = mx > m + kGaSlack || (m == -INFINITY && mx > m);
-                    any = __any_sync(0xffffffffu, raise);
-                    if (!any) break;
-                    if (raise) {
-                        f = ga_ex2(m - mx);                        // 0 for the first keys of a row
-                        m = mx;
-                    }
+                for (int i = 0; i < 16; ++i) {
+                    float2 e = ga_fma2(make_float2(x[2 * i], x[2 * i + 1]), sc, rf);
+                    e.x = ga_ex2(e.x);
+                    e.y = ga_ex2(e.y);
+                    sum = ga_add2(sum, e);
+                    p[i] = f32x2_f16x2(e.x, e.y);
                 }
-            }
-            if (kb > s.k0) {                                       // two pieces in each place
-                piece_add(std::integral_constant<int, 32>{}, 0, &sm.ds_full, &sm.ds_empty, kGaSCol, 0u);
-                piece_add(std::integral_constant<int, 16>{}, 32, &sm.dd_full, &sm.dd_empty, kGaDCol, 0u);
-                piece_add(std::integral_constant<int, 32>{}, 48, &sm.ds_full, &sm.ds_empty, kGaSCol, 1u);
-                piece_add(std::integral_constant<int, 16>{}, 80, &sm.dd_full, &sm.dd_empty, kGaDCol, 1u);
-            }
-            if (!scores) break;
-            // every MMA of the block before is done (its last piece has been read): O and P are this thread's
-            if (any) {
+                if (pass == 1) break;
+                ga_pair_bar(pair_bar);
+                mx = fmaxf(mx, sm.mx[par][half ^ 1][row]);
+                mx = mx == -INFINITY ? mx : mx * scale;
+                const bool raise = mx > m + kGaSlack || (m == -INFINITY && mx > m);
+                if (!__any_sync(0xffffffffu, raise)) break;
+                const float f = raise ? ga_ex2(m - mx) : 1.0f;     // 0 for the first keys of a row
+                if (raise) m = mx;
                 l *= f;
 #pragma unroll
                 for (int i = 0; i < kGaRegs / 2; ++i) acc[i] = make_float2(acc[i].x * f, acc[i].y * f);
-                if (kb > s.k0) {
+                if (kb > s.k0) {                                   // O of the block before is complete
 #pragma unroll 1
                     for (int c = 0; c < kGaTmemCh / 2; c += 16) {
                         float a[16];
                         uint32_t o[16];
-                        const uint32_t at = tm + ga_o_col(c, half);
+                        const uint32_t at = tm + half * (kGaTmemCh / 2) + c;
                         tmem_ld16(at, a);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(a[i] * f);
@@ -551,14 +539,19 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
                     }
                 }
             }
-            l += sum;
             ga_tmem_st16(tm + kGaPCol + 16 * half, p);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) ga_arrive_first(&sm.p_full);
+            if (lane == 0) mbar_arrive(&sm.p_full);
+            l += sum.x + sum.y;
+            piece_add(std::integral_constant<int, 32>{}, 0);
+            piece_add(std::integral_constant<int, 32>{}, 32);
+            piece_add(std::integral_constant<int, 16>{}, 64);
         }
         // ---- end of the segment
-        const int tok = tok0 + (row >> 4), h = row & 15;
+        wait(&sm.o_done, (blk - 1) & 1u);
+        tc_fence_after();
+        const int tok = row >> 4, h = row & 15;
         const bool live = tok < s.ntok;
         if (half == 1) sm.l[row] = l;
         ga_pair_bar(pair_bar);
@@ -566,23 +559,23 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
         ga_pair_bar(pair_bar);
         l = sm.l[row];
         if (s.k0 > 0 || s.k1 < s.blocks) {
-            // part of a row tile: unnormalised
-            const int64_t slot = 2 * (blockIdx.x / 2) + (seg_no > 0);
+            // part of a row tile: unnormalised, [slot][token][channel][head]
+            const int64_t slot = 2 * blockIdx.x + (seg_no > 0);
             float *po = A.part_o + (slot * A.tok_slots + tok) * (kDim * kHeads) + h;
             if (live && half == 0) A.part_ml[(slot * A.tok_slots + tok) * kHeads + h] = make_float2(m, l);
 #pragma unroll 1
             for (int c = 0; c < kGaTmemCh / 2; c += 16) {
                 float a[16];
-                tmem_ld16(tm + ga_o_col(c, half), a);
+                tmem_ld16(tm + half * (kGaTmemCh / 2) + c, a);
                 if (live)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) po[(kGaCtaCh * half + c + i) * kHeads] = a[i];
+                    for (int i = 0; i < 16; ++i) po[(half * (kGaTmemCh / 2) + c + i) * kHeads] = a[i];
             }
             if (live)
 #pragma unroll
                 for (int i = 0; i < kGaRegs / 2; ++i) {
-                    po[(kGaCtaCh * half + kGaTmemCh / 2 + 2 * i) * kHeads] = acc[i].x;
-                    po[(kGaCtaCh * half + kGaTmemCh / 2 + 2 * i + 1) * kHeads] = acc[i].y;
+                    po[(ga_reg_channel(2 * i & ~15, half) + (2 * i & 15)) * kHeads] = acc[i].x;
+                    po[(ga_reg_channel(2 * i & ~15, half) + (2 * i & 15) + 1) * kHeads] = acc[i].y;
                 }
         } else {
             // the whole row tile: join the token's own part and write it
@@ -591,163 +584,144 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
             const float top = fmaxf(m, lo), ref = top == -INFINITY ? 0.0f : top;
             const float wk = ga_ex2(m - ref), wo = ga_ex2(lo - ref);
             const float sum = l * wk + wo;
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            const float fk = wk * inv, fo = wo * inv;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;     // a NaN stays one
+            const float fk = wk * inv, fo = wo > 0.0f ? wo * inv : 0.0f;   // nothing to read without an own part
             if (live && half == 0)
                 A.lse[r] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
-            auto write = [&](int ch, const float *a) {             // 16 channels from ch on
-                float v[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = a[i] * fk;
-                if (wo > 0.0f) {
-                    const float4 *own = reinterpret_cast<const float4 *>(A.o_own + r * kDim + ch);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 o = __ldg(own + i);
-                        v[4 * i] += fo * o.x;
-                        v[4 * i + 1] += fo * o.y;
-                        v[4 * i + 2] += fo * o.z;
-                        v[4 * i + 3] += fo * o.w;
-                    }
-                }
-                uint32_t b[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                    b[i] = *reinterpret_cast<const uint32_t *>(&t);
-                }
-                uint4 *dst = reinterpret_cast<uint4 *>(A.out + r * kDim + ch);
-                dst[0] = make_uint4(b[0], b[1], b[2], b[3]);
-                dst[1] = make_uint4(b[4], b[5], b[6], b[7]);
-            };
 #pragma unroll 1
             for (int c = 0; c < kGaTmemCh / 2; c += 16) {
                 float a[16];
-                tmem_ld16(tm + ga_o_col(c, half), a);
-                if (live) write(kGaCtaCh * half + c, a);
+                tmem_ld16(tm + half * (kGaTmemCh / 2) + c, a);
+                if (live) ga_write16(A, r, half * (kGaTmemCh / 2) + c, a, fk, fo);
             }
             if (live)
 #pragma unroll
-                for (int j = 0; j < kGaRegs; j += 16) write(kGaCtaCh * half + kGaTmemCh / 2 + j, reinterpret_cast<const float *>(acc) + j);
+                for (int j = 0; j < kGaRegs; j += 16)
+                    ga_write16(A, r, ga_reg_channel(j, half), reinterpret_cast<const float *>(acc) + j, fk, fo);
         }
         tc_fence_before();
         ++seg_no;
     }
 }
 
-// Three warps of each CTA fill K and three V, each one chunk of every round: a
-// K chunk is 64 channels of this CTA's 32 keys, a V chunk 32 of
-// its channels for all 64 keys, either way two 16-byte loads per lane. The loads
-// of three chunks are in flight; one loop serves K and V, chunk by chunk (small
-// code, see GaWait). A warp passes every phase of the barriers it waits for, so
-// their parity is enough.
-struct GaRaw {
-    uint4 v[2];                        // 32 channels of two keys
-    uint32_t s[2];                     // their two scales each
-    int left;                          // keys that count from this lane's first on
-};
-
-__device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk walk, bool is_k, int place, int lane) {
-    const int rank = blockIdx.x & 1;
-    // first key and 16-byte piece of this lane; keys from its first to its second; pieces and bytes of a chunk
-    const int key = is_k ? 32 * rank + (lane & 15) : lane, piece = is_k ? lane >> 4 : 9 * rank;
-    const int step = is_k ? 16 : 32, pieces = is_k ? 2 : 1;
-    const uint32_t slab = is_k ? kGaKSlab : kGaVSlab, chunk = (is_k ? 8 : 4) * slab;
-    uint8_t *dst0 = is_k ? sm.k + 4 * (lane >> 4) * kGaKSlab + (lane & 15) * 16 : sm.v + lane * 16;
-    uint64_t *full = is_k ? sm.k_full : sm.v_full, *free_ = is_k ? sm.k_free : sm.v_free;
-    GaWait wait;
-    // ---- the fetch cursor: place at of block kb of segment s
-    GaSeg s = {};
-    int kb = 0, page = 0, left = 0, at = place;
-    const uint8_t *codes = nullptr, *scales = nullptr;
-    auto segment = [&]() {                                         // the next one with entries
+// Walks the blocks of a range's segments with entries, one ahead with the page.
+struct GaBlocks {
+    GaWalk walk;
+    GaSeg s;
+    int kb, page;                      // the block at hand; its page
+    __device__ __forceinline__ bool segment(const GaArgs &A) {
         do {
             if (!walk.next(A, s)) return false;
         } while (s.T == 0);
         kb = s.k0;
         page = __ldg(A.page_table + static_cast<int64_t>(s.g) * A.max_pages + kb);
         return true;
-    };
-    auto open = [&]() {                                            // block kb, whose page has been read
-        left = s.T - kb * kGaBlk - key;
-        if (page < 0 || page >= A.num_pages) {
-            flag_status(kStatusBounds);
-            left = 0;
-            page = 0;
-        }
-        const int64_t slot = static_cast<int64_t>(page) * kPage + key;
-        codes = A.kv_fp4 + slot * kFp4Bytes + 16 * piece;
-        scales = A.kv_scale + slot * kScaleBytes + 2 * piece;
+    }
+    // The page of the block at hand (-1: none); moves the page on to the next block of the segment.
+    __device__ __forceinline__ int take(const GaArgs &A) {
+        const int now = page >= 0 && page < A.num_pages ? page : -1;
         if (kb + 1 < s.k1) page = __ldg(A.page_table + static_cast<int64_t>(s.g) * A.max_pages + kb + 1);
+        return now;
+    }
+    __device__ __forceinline__ bool next(const GaArgs &A) { return ++kb < s.k1 || segment(A); }
+};
+
+// Six warps each fill the same half (32 keys) of one chunk of every round, two
+// 16-byte loads per lane. A round's loads for the next block are issued as soon
+// as it has been converted, so they have a block's time; with one round less in
+// flight each round waited for L2 (900 cycles). A warp passes every phase of the
+// barriers it waits for, so their parity is enough.
+struct GaRaw {
+    uint4 v[2];                        // 32 channels of two keys
+    uint32_t s[2];                     // their two scales each
+};
+
+__device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk walk, int warp, int lane) {
+    const int place = warp % 3, key = 32 * (warp / 3) + (lane & 15), part = lane >> 4;   // the lane's first key, and 16 on
+    uint8_t *const dst0 = sm.k + 4 * part * kGaKSlab + key * 16;
+    auto chunk_of = [&](int round) { return place < 2 ? 2 * round + place : ga_third_chunk(round); };
+    const uint8_t *codes = nullptr, *scales = nullptr;
+    GaWait wait;
+    GaBlocks b = {walk, {}, 0, 0};
+    int left = 0;
+    auto open = [&]() {                                            // the block at hand
+        const int page = b.take(A);
+        if (page < 0 && b.s.T > b.kb * kGaBlk) flag_status(kStatusBounds);
+        left = page < 0 ? 0 : b.s.T - b.kb * kGaBlk - key;
+        const int64_t slot = static_cast<int64_t>(max(page, 0)) * kPage + key;
+        codes = A.kv_fp4 + slot * kFp4Bytes + 16 * part;
+        scales = A.kv_scale + slot * kScaleBytes + 2 * part;
     };
-    bool more = segment();
-    if (!more) return;
-    open();
-    auto fetch = [&](GaRaw &r) {
-        r.left = left;
-        const int off = at * pieces;
+    GaRaw raw[kGaRounds];
+    auto fetch = [&](int i) {
+        const int c = chunk_of(i);
         // unconditional, so that nothing waits for them here: the rows are in the page whether they count or not
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            r.v[k] = __ldg(reinterpret_cast<const uint4 *>(codes + k * step * kFp4Bytes + 16 * off));
-            r.s[k] = __ldg(reinterpret_cast<const uint16_t *>(scales + k * step * kScaleBytes + 2 * off));
-        }
-        at += kGaCrew;
-        if (at >= kGaChunks) {                                     // the next block; at the end the last one again, unused
-            at = place;
-            if (++kb == s.k1) more = segment();
-            if (more) open();
+            raw[i].v[k] = __ldg(reinterpret_cast<const uint4 *>(codes + 16 * k * kFp4Bytes + 32 * c));
+            raw[i].s[k] = __ldg(reinterpret_cast<const uint16_t *>(scales + 16 * k * kScaleBytes + 4 * c));
         }
     };
-    GaRaw r0, r1, r2;
-    int todo = 0;                                                  // chunks fetched and not converted
-    fetch(r0);
-    fetch(r1);
-    fetch(r2);
-    todo = 3;
-    int round = 0;
-    uint32_t blk = 0;
-#pragma unroll 1
-    while (todo > 0) {
-        if (blk > 0) wait(&free_[round], (blk - 1) & 1u);
-        uint8_t *dst = dst0 + (round * kGaCrew + place) * chunk;
+    bool more = b.segment(A);
+    if (!more) return;
+    open();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (r0.left <= k * step) {                             // entries that do not count are zeros
-                r0.v[k] = make_uint4(0u, 0u, 0u, 0u);
-                r0.s[k] = 0u;
-            }
-            const uint32_t s2 = e4m3x2_to_f16x2(r0.s[k]);
-            const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
+    for (int i = 0; i < kGaRounds; ++i) fetch(i);
+    uint32_t phase = 1u;                                           // of free: passes at once for the first block
+    while (more) {
+        const int count = left;                                    // keys that count from this lane's first on
+        more = b.next(A);
+        if (more) open();
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const uint32_t w = (&r0.v[k].x)[v], f = v < 2 ? sa : sb;
-                *reinterpret_cast<uint4 *>(dst + v * slab + k * step * 16) = make_uint4(
-                    hmul2_u32(e2m1x2_to_f16x2(w & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2((w >> 8) & 0xffu), f),
-                    hmul2_u32(e2m1x2_to_f16x2((w >> 16) & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2(w >> 24), f));
+        for (int i = 0; i < kGaRounds; ++i) {
+            GaRaw &r = raw[i];
+            wait(&sm.k_free[i], phase);
+            uint8_t *dst = dst0 + chunk_of(i) * (8 * kGaKSlab);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const bool ok = count > 16 * k;                    // entries that do not count are zeros
+                const uint32_t s2 = ok ? e4m3x2_to_f16x2(r.s[k]) : 0u;
+                const uint32_t sa = __byte_perm(s2, s2, 0x1010), sb = __byte_perm(s2, s2, 0x3232);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint32_t w = (&r.v[k].x)[v], f = v < 2 ? sa : sb;
+                    *reinterpret_cast<uint4 *>(dst + v * kGaKSlab + k * 256) = make_uint4(
+                        hmul2_u32(e2m1x2_to_f16x2(w & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2((w >> 8) & 0xffu), f),
+                        hmul2_u32(e2m1x2_to_f16x2((w >> 16) & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2(w >> 24), f));
+                }
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.k_full[i]);
+            if (more) fetch(i);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ga_arrive_first(&full[round]);
-        r0 = r1;
-        r1 = r2;
-        if (more) fetch(r2);
-        else --todo;
-        if (++round == kGaRounds) {
-            round = 0;
-            ++blk;
-        }
+        phase ^= 1u;
     }
 }
 
-// The tensor memory address is 0: all of it is allocated. The pair's MMAs take
-// 128 rows from each CTA and half of B's columns. K-major operands: leading
-// offset along K (8 channels), stride offset along the rows; MN-major (V):
-// along the keys, along the channels.
+// Brings the pages of the blocks ahead to L2, at the pace of the first round.
+__device__ __forceinline__ void ga_prefetch(const GaArgs &A, GaSmem &sm, GaWalk walk, int lane) {
+    constexpr int kAhead = 4;
+    GaWait wait;
+    GaBlocks b = {walk, {}, 0, 0};
+    int n = 0;
+    for (bool more = b.segment(A); more; more = b.next(A), ++n) {
+        if (n >= kAhead) wait(&sm.k_free[0], (n - kAhead) & 1u);
+        const int page = b.take(A);
+        if (page < 0 || lane > 0) continue;
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                     ::"l"(A.kv_fp4 + static_cast<int64_t>(page) * (kPage * kFp4Bytes)), "r"(kPage * kFp4Bytes) : "memory");
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                     ::"l"(A.kv_scale + static_cast<int64_t>(page) * (kPage * kScaleBytes)), "r"(kPage * kScaleBytes) : "memory");
+    }
+}
+
+// The tensor memory address is 0: all of it is allocated. K-major operands:
+// leading offset along K (8 channels), stride offset along the rows; MN-major
+// (V): along the keys, along the channels.
 template <int kN, int kCh, int kCol>
 __device__ __forceinline__ void ga_pv(uint32_t one, uint32_t v_lo, uint32_t accumulate) {
-    constexpr uint32_t id = umma_idesc(2 * kGaRows, kN, false, true), at = kCh / 8 * kGaVSlab >> 4, hi = ga_desc_hi(kGaVSlab);
+    constexpr uint32_t id = umma_idesc(kGaRows, kN, false, true), at = kCh / 8 * kGaKSlab >> 4, hi = ga_desc_hi(kGaKSlab);
     ga_mma_ts<kCol, id, kGaPCol, at, hi>(one, v_lo, accumulate);
     ga_mma_ts<kCol, id, kGaPCol + 8, at + 16, hi>(one, v_lo, 1u);
     ga_mma_ts<kCol, id, kGaPCol + 16, at + 32, hi>(one, v_lo, 1u);
@@ -756,109 +730,84 @@ __device__ __forceinline__ void ga_pv(uint32_t one, uint32_t v_lo, uint32_t accu
 
 __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk) {
     const uint32_t one = ga_elect() ? 1u : 0u;
-    const uint32_t d_q = ga_desc_lo(sm.q, kGaQSlab), d_k = ga_desc_lo(sm.k, kGaKSlab), d_v = ga_desc_lo(sm.v, 128);
+    const uint32_t d_q = ga_desc_lo(sm.q, kGaQSlab), d_k = ga_desc_lo(sm.k, kGaKSlab), d_v = ga_desc_lo(sm.k, 128);
     GaWait wait;
-    uint32_t s_blk = 0, o_blk = 0, tile_no = 0;                    // S products, O products and tiles so far
+    uint32_t blk = 0, piece = 0, tile_no = 0;
     GaSeg s;
     while (walk.next(A, s)) {
         if (s.T == 0) continue;
         wait(&sm.q_full, tile_no & 1u);
         ++tile_no;
-        const int n = s.k1 - s.k0;
-        for (int t = 0; t <= n; ++t) {
-            const bool scores = t < n, output = t > 0;
-            const uint32_t acc = t > 1, kp = s_blk & 1u, vp = o_blk & 1u;
-            if (scores) {
-                // S's columns: the last piece there has been read (and the scores before it, see below)
-                if (o_blk > 0) ga_wait2(wait, &sm.ds_empty, 1u, &sm.k_full[0], kp);
-                else wait(&sm.k_full[0], kp);
-                constexpr uint32_t id = umma_idesc(2 * kGaRows, kGaBlk, false, false), hi = ga_desc_hi(128);
-                constexpr uint32_t da = 2 * kGaQSlab >> 4, db = 2 * kGaKSlab >> 4;      // 16 channels
-                uint32_t a = d_q, b = d_k;
+        for (int kb = s.k0; kb < s.k1; ++kb, ++blk) {
+            const uint32_t par = blk & 1u, acc = kb > s.k0;
+            constexpr uint32_t id = umma_idesc(kGaRows, kGaBlk, false, false), hi = ga_desc_hi(128);
+            constexpr uint32_t da = 2 * kGaQSlab >> 4, db = 2 * kGaKSlab >> 4;          // 16 channels
+            // S takes the columns of the pieces: the last one has been read
+            if (blk > 0) ga_wait2(wait, &sm.d_empty, (piece - 1) & 1u, &sm.k_full[0], par);
+            else wait(&sm.k_full[0], par);
 #pragma unroll 1
-                for (int i = 0; i < kGaRounds; ++i) {
-                    if (i > 0) wait(&sm.k_full[i], kp);
-                    tc_fence_after();
-                    ga_mma_ss<kGaSCol, id, 0, hi, 0, hi>(one, a, b, i > 0);
-                    ga_mma_ss<kGaSCol, id, da, hi, db, hi>(one, a, b, 1u);
-                    ga_mma_ss<kGaSCol, id, 2 * da, hi, 2 * db, hi>(one, a, b, 1u);
-                    ga_mma_ss<kGaSCol, id, 3 * da, hi, 3 * db, hi>(one, a, b, 1u);
-                    ga_mma_ss<kGaSCol, id, 4 * da, hi, 4 * db, hi>(one, a, b, 1u);
-                    ga_mma_ss<kGaSCol, id, 5 * da, hi, 5 * db, hi>(one, a, b, 1u);
-                    ga_mma_ss<kGaSCol, id, 6 * da, hi, 6 * db, hi>(one, a, b, 1u);
-                    ga_mma_ss<kGaSCol, id, 7 * da, hi, 7 * db, hi>(one, a, b, 1u);
-                    ga_mma_ss<kGaSCol, id, 8 * da, hi, 8 * db, hi>(one, a, b, 1u);
-                    ga_mma_ss<kGaSCol, id, 9 * da, hi, 9 * db, hi>(one, a, b, 1u);
-                    ga_mma_ss<kGaSCol, id, 10 * da, hi, 10 * db, hi>(one, a, b, 1u);
-                    ga_mma_ss<kGaSCol, id, 11 * da, hi, 11 * db, hi>(one, a, b, 1u);
-                    ga_commit(one, &sm.k_free[i]);
-                    a += 12 * da;
-                    b += 12 * db;
-                }
-                ga_commit(one, &sm.s_full);
-            } else if (o_blk > 0) {
-                wait(&sm.ds_empty, 1u);
+            for (int r = 0; r < kGaRounds; ++r) {
+                if (r > 0) wait(&sm.k_full[r], par);
+                tc_fence_after();
+                const uint32_t a = d_q + r * (8 * da), b = d_k + r * (8 * db);
+                const uint32_t a3 = d_q + ga_third_chunk(r) * (4 * da), b3 = d_k + ga_third_chunk(r) * (4 * db);
+                ga_mma_ss<kGaSCol, id, 0, hi, 0, hi>(one, a, b, r > 0);
+                ga_mma_ss<kGaSCol, id, da, hi, db, hi>(one, a, b, 1u);
+                ga_mma_ss<kGaSCol, id, 2 * da, hi, 2 * db, hi>(one, a, b, 1u);
+                ga_mma_ss<kGaSCol, id, 3 * da, hi, 3 * db, hi>(one, a, b, 1u);
+                ga_mma_ss<kGaSCol, id, 4 * da, hi, 4 * db, hi>(one, a, b, 1u);
+                ga_mma_ss<kGaSCol, id, 5 * da, hi, 5 * db, hi>(one, a, b, 1u);
+                ga_mma_ss<kGaSCol, id, 6 * da, hi, 6 * db, hi>(one, a, b, 1u);
+                ga_mma_ss<kGaSCol, id, 7 * da, hi, 7 * db, hi>(one, a, b, 1u);
+                ga_mma_ss<kGaSCol, id, 0, hi, 0, hi>(one, a3, b3, 1u);
+                ga_mma_ss<kGaSCol, id, da, hi, db, hi>(one, a3, b3, 1u);
+                ga_mma_ss<kGaSCol, id, 2 * da, hi, 2 * db, hi>(one, a3, b3, 1u);
+                ga_mma_ss<kGaSCol, id, 3 * da, hi, 3 * db, hi>(one, a3, b3, 1u);
             }
-            if (output) {
-                ga_wait2(wait, &sm.p_full, vp, &sm.v_full[0], vp);
-                tc_fence_after();
-                ga_pv<128, 0, 0>(one, d_v, acc);
-                wait(&sm.v_full[1], vp);
-                tc_fence_after();
-                ga_pv<128, 64, 128>(one, d_v, acc);
-                ga_commit(one, &sm.v_free[0]);
-            }
-            if (scores) {
-                wait(&sm.s_read, kp);                              // the scores are in registers: their columns are free
-                ++s_blk;
-            }
-            if (output) {
-                // the pieces, 64 columns of S's and 32 of their own, twice, each read while the next are multiplied
-                if (o_blk > 0) ga_wait2(wait, &sm.v_full[2], vp, &sm.dd_empty, 1u);
-                else wait(&sm.v_full[2], vp);
-                tc_fence_after();
-                ga_pv<64, 192, kGaSCol>(one, d_v, 0u);
-                ga_commit(one, &sm.ds_full);
-                ga_pv<32, 224, kGaDCol>(one, d_v, 0u);
-                ga_commit(one, &sm.dd_full);
-                ga_pv<128, 128, 256>(one, d_v, acc);
-                ga_commit(one, &sm.v_free[1]);
-                wait(&sm.ds_empty, 0u);
-                tc_fence_after();
-                ga_pv<64, 240, kGaSCol>(one, d_v, 0u);
-                ga_commit(one, &sm.ds_full);
-                wait(&sm.dd_empty, 0u);
-                tc_fence_after();
-                ga_pv<32, 272, kGaDCol>(one, d_v, 0u);
-                ga_commit(one, &sm.dd_full);
-                ga_commit(one, &sm.v_free[2]);
-                ++o_blk;
-            }
+            ga_commit(one, &sm.s_full);
+            wait(&sm.p_full, par);
+            tc_fence_after();
+            // O in parts of 128, 128 and 160 channels between the pieces of 64, 64 and 32 (channels 416, 480 and
+            // 544 on), so that a piece is read while a part is multiplied
+            ga_pv<64, 416, kGaSCol>(one, d_v, 0u);
+            ga_commit(one, &sm.d_full);
+            ga_pv<128, 0, 0>(one, d_v, acc);
+            wait(&sm.d_empty, piece & 1u);
+            tc_fence_after();
+            ga_pv<64, 480, kGaSCol>(one, d_v, 0u);
+            ga_commit(one, &sm.d_full);
+            ga_commit(one, &sm.k_free[0]);                         // chunks 0, 1 and 7
+            ga_pv<128, 128, 128>(one, d_v, acc);
+            wait(&sm.d_empty, (piece + 1) & 1u);
+            tc_fence_after();
+            ga_pv<32, 544, kGaSCol>(one, d_v, 0u);
+            ga_commit(one, &sm.d_full);
+            ga_commit(one, &sm.k_free[1]);                         // 2, 3 and 8
+            ga_pv<160, 256, 256>(one, d_v, acc);
+            ga_commit(one, &sm.k_free[2]);                         // 4, 5 and 6
+            ga_commit(one, &sm.o_done);
+            piece += 3;
         }
     }
-    // every MMA of the pair is done before tensor memory goes back
-    if (o_blk > 0) wait(&sm.dd_full, 1u);
+    // every MMA of this CTA is done before tensor memory goes back
+    if (blk > 0) wait(&sm.o_done, (blk - 1) & 1u);
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGaThreads, 1)
+__global__ void __launch_bounds__(kGaThreads, 1)
 group_attn_kernel(const GaArgs A) {
     extern __shared__ __align__(1024) uint8_t ga_raw[];
     GaSmem &sm = *reinterpret_cast<GaSmem *>(ga_raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, range = blockIdx.x / 2;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, range = blockIdx.x;
     if (tid == 0) {
-        mbar_init(&sm.q_full, 2);
+        mbar_init(&sm.q_full, 1);
         mbar_init(&sm.s_full, 1);
-        mbar_init(&sm.s_read, 2 * kGaSoftWarps);
-        mbar_init(&sm.p_full, 2 * kGaSoftWarps);
-        mbar_init(&sm.ds_full, 1);
-        mbar_init(&sm.ds_empty, 2 * kGaSoftWarps);
-        mbar_init(&sm.dd_full, 1);
-        mbar_init(&sm.dd_empty, 2 * kGaSoftWarps);
+        mbar_init(&sm.p_full, kGaSoftWarps);
+        mbar_init(&sm.d_full, 1);
+        mbar_init(&sm.d_empty, kGaSoftWarps);
+        mbar_init(&sm.o_done, 1);
         for (int i = 0; i < kGaRounds; ++i) {
-            mbar_init(&sm.k_full[i], 2 * kGaCrew);
-            mbar_init(&sm.v_full[i], 2 * kGaCrew);
+            mbar_init(&sm.k_full[i], kGaDeqWarps);
             mbar_init(&sm.k_free[i], 1);
-            mbar_init(&sm.v_free[i], 1);
         }
         fence_mbar_init();
     }
@@ -866,12 +815,12 @@ group_attn_kernel(const GaArgs A) {
     ga_locate(A, sm);
     __syncthreads();
     const int64_t total = sm.total;
-    const int ranges = static_cast<int>(min(static_cast<int64_t>(gridDim.x / 2), total));
-    if (blockIdx.x == 0 && tid == 0) {
+    const int ranges = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    if (range == 0 && tid == 0) {
         A.plan->total = total;
         A.plan->ranges = ranges;
     }
-    if (range >= ranges) return;                                   // both CTAs of the pair
+    if (range >= ranges) return;
     if (tid == 0) {
         const int64_t at = ga_range(total, range, ranges), local = at - sm.start;
         const GaGroup grp = ga_group(A, sm.start_g, false);
@@ -882,21 +831,18 @@ group_attn_kernel(const GaArgs A) {
         w.tile = static_cast<int>(local / len);
         w.k = static_cast<int>(local - static_cast<int64_t>(w.tile) * len);
         sm.walk = w;
-        if ((blockIdx.x & 1) == 0) {
-            GaPlan::Tile &t = A.plan->first[range];
-            t.begin = at - w.k + kGaGap;
-            t.blocks = grp.blocks;
-            t.tok0 = grp.tok0 + w.tile * kGaTok;
-            t.ntok = min(kGaTok, grp.n - w.tile * kGaTok);
-        }
+        GaPlan::Tile &t = A.plan->first[range];
+        t.begin = at - w.k + kGaGap;
+        t.blocks = grp.blocks;
+        t.tok0 = grp.tok0 + w.tile * kGaTok;
+        t.ntok = min(kGaTok, grp.n - w.tile * kGaTok);
     }
     if (warp == kGaMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        tmem_alloc(&sm.tmem, 512);
+        tmem_relinquish();
         tc_fence_before();
     }
     __syncthreads();
-    ga_cluster_sync();                                             // barriers and tensor memory of both CTAs
     tc_fence_after();
     const GaWalk walk = sm.walk;
     if (warp < kGaSoftWarps) {
@@ -904,20 +850,20 @@ group_attn_kernel(const GaArgs A) {
         ga_softmax(A, sm, walk, warp, lane);
     } else {
         ga_regs_down<kGaOtherRegs>();
-        if (warp == kGaMmaWarp) {
-            if ((blockIdx.x & 1) == 0) ga_mma(A, sm, walk);
-        } else if (warp < kGaVWarp + kGaCrew) {
-            ga_dequant(A, sm, walk, warp < kGaVWarp, (warp - kGaKWarp) % kGaCrew, lane);
-        }
+        if (warp == kGaMmaWarp)
+            ga_mma(A, sm, walk);
+        else if (warp < kGaDeqWarp + kGaDeqWarps)
+            ga_dequant(A, sm, walk, warp - kGaDeqWarp, lane);
+        else
+            ga_prefetch(A, sm, walk, lane);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    ga_cluster_sync();                                             // no arrival is on its way to a CTA that has ended
     pdl_trigger();
     if (warp == kGaMmaWarp) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
+        tmem_dealloc(sm.tmem, 512);
     }
 }
 
@@ -931,14 +877,14 @@ group_attn_kernel(const GaArgs A) {
 constexpr int kGmThreads = 256;
 
 struct GmSmem {
-    float w[kGaMaxPairs + 1][kHeads];                               // weight of a partial
+    float w[kGaMaxCtas + 1][kHeads];                               // weight of a partial
     float red[kGmThreads / kHeads][kHeads];
     union {
         float4 sum[4][64];
         alignas(16) uint16_t out[kHeads][kDim + 8];
     };
     float inv[kHeads], fo[kHeads];
-    int first[kGaMaxPairs + 1];                                     // units before the c-th boundary's tile
+    int first[kGaMaxCtas + 1];                                     // units before the c-th boundary's tile
     int warp_sum[kGmThreads / 32];
 };
 
@@ -950,7 +896,7 @@ struct GmTile {
 
 __device__ __forceinline__ void gm_weights(const GaArgs &A, GmSmem &sm, const GmTile &t, int tok, int64_t row, bool first) {
     const int tid = threadIdx.x, h = tid & (kHeads - 1), at = tid >> 4;
-    constexpr int kLanes = kGmThreads / kHeads, kMost = (kGaMaxPairs + kLanes) / kLanes;
+    constexpr int kLanes = kGmThreads / kHeads, kMost = (kGaMaxCtas + kLanes) / kLanes;
     float2 ml[kMost];
     float own = -INFINITY;
     if (A.lse_own) own = __ldg(A.lse_own + row + h) * 1.4426950408889634f;
@@ -1082,16 +1028,16 @@ group_attn_merge_kernel(const GaArgs A) {
     if (lane == 31) sm.warp_sum[warp] = incl;
     __syncthreads();
     for (int w = 0; w < warp; ++w) incl += sm.warp_sum[w];
-    if (tid < kGaMaxPairs) sm.first[tid + 1] = incl;                // tokens up to boundary tid
+    if (tid < kGaMaxCtas) sm.first[tid + 1] = incl;                // tokens up to boundary tid
     if (tid == 0) sm.first[0] = 0;
     __syncthreads();
-    const int tokens = sm.first[kGaMaxPairs];
+    const int tokens = sm.first[kGaMaxCtas];
     // slices of 16 channels while 36 of them per token fit one wave of CTAs, then of 64, then whole tokens
     const int grid = static_cast<int>(gridDim.x);
     const int per = tokens * 36 <= grid ? 36 : tokens * 9 <= 2 * grid ? 9 : 1;
     for (int unit = blockIdx.x; unit < tokens * per; unit += grid) {
         const int ut = unit / per, slice = unit - ut * per;
-        int lo = 0, hi = kGaMaxPairs;                               // the boundary: first[c] <= ut < first[c + 1]
+        int lo = 0, hi = kGaMaxCtas;                               // the boundary: first[c] <= ut < first[c + 1]
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (sm.first[mid] <= ut) lo = mid; else hi = mid;
@@ -1113,9 +1059,9 @@ group_attn_merge_kernel(const GaArgs A) {
 
 // Workspace: the plan, then two partials per range.
 inline size_t ga_plan_bytes() { return (sizeof(GaPlan) + 255) / 256 * 256; }
-inline size_t ga_ml_bytes(int tok_slots) { return static_cast<size_t>(2 * kGaMaxPairs) * tok_slots * kHeads * sizeof(float2); }
+inline size_t ga_ml_bytes(int tok_slots) { return static_cast<size_t>(2 * kGaMaxCtas) * tok_slots * kHeads * sizeof(float2); }
 inline size_t ga_ws_bytes(int tok_slots) {
-    return ga_plan_bytes() + ga_ml_bytes(tok_slots) + static_cast<size_t>(2 * kGaMaxPairs) * tok_slots * kHeads * kDim * 4;
+    return ga_plan_bytes() + ga_ml_bytes(tok_slots) + static_cast<size_t>(2 * kGaMaxCtas) * tok_slots * kHeads * kDim * 4;
 }
 
 }  // namespace csa2
