@@ -60,16 +60,16 @@ constexpr int kGaThreads = 16 * 32;                                // 512: whole
 constexpr int kGaSoftRegs = 168, kGaOtherRegs = 88;
 constexpr int kGaChunk = 64;                                       // channels per chunk
 constexpr int kGaQSlab = kGaRows * 16, kGaKSlab = kGaBlk * 16;     // 2,048 and 1,024 B: 8 channels of every row
-constexpr int kGaTmemCh = 416;                                     // channels accumulated in tensor memory
-constexpr int kGaSCol = kGaTmemCh, kGaPCol = kGaSCol + kGaBlk;     // 416, 480
-constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a softmax thread holds: 80
+constexpr int kGaTmemCh = 384;                                     // channels accumulated in tensor memory
+constexpr int kGaSCol = kGaTmemCh, kGaDCol = kGaSCol + kGaBlk;     // 384, 448
+constexpr int kGaPCol = kGaDCol + 32;                              // 480
+constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a softmax thread holds: 96
 // A block's nine chunks are filled, multiplied and released in three rounds, in
-// the order in which O's MMAs are done with them: 0 1 7, 2 3 8, 4 5 6.
+// the order in which O's MMAs are done with them: 2 r, 2 r + 1 and 6 + r.
 constexpr int kGaRounds = 3;
-__device__ __forceinline__ int ga_third_chunk(int round) { return round == 2 ? 6 : 7 + round; }
 constexpr int kGaGap = 2;                                          // steps a row tile counts for beside its blocks
 constexpr float kGaSlack = 8.0f;                                   // log2 units a block may exceed the reference
-static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 80, "tensor memory is full; pieces of 64, 64 and 32 channels");
+static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 96, "tensor memory is full; pieces of 64, 32, 64 and 32 channels");
 
 struct GaArgs {
     const __nv_bfloat16 *q;            // [N][16][576]
@@ -172,7 +172,8 @@ struct GaSmem {
     uint64_t q_full;                   // query tile in
     uint64_t s_full;                   // scores in tensor memory
     uint64_t p_full;                   // probabilities in tensor memory, O rescaled
-    uint64_t d_full, d_empty;          // a piece in S's columns; read
+    uint64_t ds_full, ds_empty;        // a piece in S's columns; read
+    uint64_t dd_full, dd_empty;        // a piece in its own 32 columns; read
     uint64_t o_done;                   // a block's O is complete
     uint64_t k_full[kGaRounds], k_free[kGaRounds];
     uint32_t tmem;
@@ -407,9 +408,9 @@ __device__ __forceinline__ void ga_own_only(const GaArgs &A, const GaSeg &s, int
 }
 
 // Channel of a softmax thread's output register i (a multiple of 16): pieces
-// of 64, 64 and 32 channels, half of each.
+// of 64, 32, 64 and 32 channels from 384 on, half of each.
 __device__ __forceinline__ constexpr int ga_reg_channel(int i, int half) {
-    return i < 64 ? kGaTmemCh + (i & 32) * 2 + half * 32 + (i & 16) : kGaTmemCh + 128 + half * 16;
+    return i < 32 ? 384 + 32 * half + i : i < 48 ? 448 + 16 * half : i < 80 ? 480 + 32 * half + i - 48 : 544 + 16 * half;
 }
 
 // 16 channels of a row's result from ch on: the entries' sums times fk, the own part times fo.
@@ -444,7 +445,7 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
     const uint32_t tm = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int pair_bar = 1 + (warp & 3);                           // the two warps of the same rows
     GaWait wait;
-    uint32_t blk = 0, piece = 0, seg_no = 0;
+    uint32_t blk = 0, seg_no = 0;
     GaSeg s;
     while (walk.next(A, s)) {
         if (s.T == 0) {
@@ -464,19 +465,18 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
 #pragma unroll
         for (int i = 0; i < kGaRegs / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
         // adds this half's columns of a piece
-        auto piece_add = [&](auto n_, int to) {
+        auto piece_add = [&](auto n_, int to, uint64_t *full, uint64_t *empty, int col, uint32_t parity) {
             constexpr int kN = decltype(n_)::value;
-            wait(&sm.d_full, piece & 1u);
-            ++piece;
+            wait(full, parity);
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < kN; c += 16) {
                 float a[16];
-                tmem_ld16(tm + kGaSCol + kN * half + c, a);
+                tmem_ld16(tm + col + kN * half + c, a);
                 if (c + 16 == kN) {                                // the columns are free
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.d_empty);
+                    if (lane == 0) mbar_arrive(empty);
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -544,9 +544,10 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_full);
             l += sum.x + sum.y;
-            piece_add(std::integral_constant<int, 32>{}, 0);
-            piece_add(std::integral_constant<int, 32>{}, 32);
-            piece_add(std::integral_constant<int, 16>{}, 64);
+            piece_add(std::integral_constant<int, 32>{}, 0, &sm.ds_full, &sm.ds_empty, kGaSCol, 0u);
+            piece_add(std::integral_constant<int, 16>{}, 32, &sm.dd_full, &sm.dd_empty, kGaDCol, 0u);
+            piece_add(std::integral_constant<int, 32>{}, 48, &sm.ds_full, &sm.ds_empty, kGaSCol, 1u);
+            piece_add(std::integral_constant<int, 16>{}, 80, &sm.dd_full, &sm.dd_empty, kGaDCol, 1u);
         }
         // ---- end of the segment
         wait(&sm.o_done, (blk - 1) & 1u);
@@ -631,6 +632,13 @@ struct GaBlocks {
 // as it has been converted, so they have a block's time; with one round less in
 // flight each round waited for L2 (900 cycles). A warp passes every phase of the
 // barriers it waits for, so their parity is enough.
+// Eight E2M1 codes of a word -> four f16x2, without moving the bytes apart first.
+__device__ __forceinline__ void ga_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
 struct GaRaw {
     uint4 v[2];                        // 32 channels of two keys
     uint32_t s[2];                     // their two scales each
@@ -639,7 +647,7 @@ struct GaRaw {
 __device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk walk, int warp, int lane) {
     const int place = warp % 3, key = 32 * (warp / 3) + (lane & 15), part = lane >> 4;   // the lane's first key, and 16 on
     uint8_t *const dst0 = sm.k + 4 * part * kGaKSlab + key * 16;
-    auto chunk_of = [&](int round) { return place < 2 ? 2 * round + place : ga_third_chunk(round); };
+    auto chunk_of = [&](int round) { return place < 2 ? 2 * round + place : 6 + round; };
     const uint8_t *codes = nullptr, *scales = nullptr;
     GaWait wait;
     GaBlocks b = {walk, {}, 0, 0};
@@ -685,9 +693,10 @@ __device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk w
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const uint32_t w = (&r.v[k].x)[v], f = v < 2 ? sa : sb;
-                    *reinterpret_cast<uint4 *>(dst + v * kGaKSlab + k * 256) = make_uint4(
-                        hmul2_u32(e2m1x2_to_f16x2(w & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2((w >> 8) & 0xffu), f),
-                        hmul2_u32(e2m1x2_to_f16x2((w >> 16) & 0xffu), f), hmul2_u32(e2m1x2_to_f16x2(w >> 24), f));
+                    uint32_t h[4];
+                    ga_e2m1x8(w, h);
+                    *reinterpret_cast<uint4 *>(dst + v * kGaKSlab + k * 256) =
+                        make_uint4(hmul2_u32(h[0], f), hmul2_u32(h[1], f), hmul2_u32(h[2], f), hmul2_u32(h[3], f));
                 }
             }
             fence_proxy_async_smem();
@@ -732,7 +741,7 @@ __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk)
     const uint32_t one = ga_elect() ? 1u : 0u;
     const uint32_t d_q = ga_desc_lo(sm.q, kGaQSlab), d_k = ga_desc_lo(sm.k, kGaKSlab), d_v = ga_desc_lo(sm.k, 128);
     GaWait wait;
-    uint32_t blk = 0, piece = 0, tile_no = 0;
+    uint32_t blk = 0, tile_no = 0;
     GaSeg s;
     while (walk.next(A, s)) {
         if (s.T == 0) continue;
@@ -742,15 +751,15 @@ __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk)
             const uint32_t par = blk & 1u, acc = kb > s.k0;
             constexpr uint32_t id = umma_idesc(kGaRows, kGaBlk, false, false), hi = ga_desc_hi(128);
             constexpr uint32_t da = 2 * kGaQSlab >> 4, db = 2 * kGaKSlab >> 4;          // 16 channels
-            // S takes the columns of the pieces: the last one has been read
-            if (blk > 0) ga_wait2(wait, &sm.d_empty, (piece - 1) & 1u, &sm.k_full[0], par);
+            // S's columns: the last piece there has been read
+            if (blk > 0) ga_wait2(wait, &sm.ds_empty, 1u, &sm.k_full[0], par);
             else wait(&sm.k_full[0], par);
 #pragma unroll 1
             for (int r = 0; r < kGaRounds; ++r) {
                 if (r > 0) wait(&sm.k_full[r], par);
                 tc_fence_after();
                 const uint32_t a = d_q + r * (8 * da), b = d_k + r * (8 * db);
-                const uint32_t a3 = d_q + ga_third_chunk(r) * (4 * da), b3 = d_k + ga_third_chunk(r) * (4 * db);
+                const uint32_t a3 = d_q + (6 + r) * (4 * da), b3 = d_k + (6 + r) * (4 * db);
                 ga_mma_ss<kGaSCol, id, 0, hi, 0, hi>(one, a, b, r > 0);
                 ga_mma_ss<kGaSCol, id, da, hi, db, hi>(one, a, b, 1u);
                 ga_mma_ss<kGaSCol, id, 2 * da, hi, 2 * db, hi>(one, a, b, 1u);
@@ -767,26 +776,31 @@ __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk)
             ga_commit(one, &sm.s_full);
             wait(&sm.p_full, par);
             tc_fence_after();
-            // O in parts of 128, 128 and 160 channels between the pieces of 64, 64 and 32 (channels 416, 480 and
-            // 544 on), so that a piece is read while a part is multiplied
-            ga_pv<64, 416, kGaSCol>(one, d_v, 0u);
-            ga_commit(one, &sm.d_full);
+            // O in parts of 128 channels between the pieces (64 columns of S's and 32 of their own, twice), so that
+            // 400 cycles of other MMAs lie between a piece and the next use of its columns
+            ga_pv<64, 384, kGaSCol>(one, d_v, 0u);
+            ga_commit(one, &sm.ds_full);
+            if (blk > 0) {
+                wait(&sm.dd_empty, 1u);
+                tc_fence_after();
+            }
+            ga_pv<32, 448, kGaDCol>(one, d_v, 0u);
+            ga_commit(one, &sm.dd_full);
             ga_pv<128, 0, 0>(one, d_v, acc);
-            wait(&sm.d_empty, piece & 1u);
+            ga_commit(one, &sm.k_free[0]);                         // chunks 0, 1 and 6
+            wait(&sm.ds_empty, 0u);
             tc_fence_after();
             ga_pv<64, 480, kGaSCol>(one, d_v, 0u);
-            ga_commit(one, &sm.d_full);
-            ga_commit(one, &sm.k_free[0]);                         // chunks 0, 1 and 7
+            ga_commit(one, &sm.ds_full);
             ga_pv<128, 128, 128>(one, d_v, acc);
-            wait(&sm.d_empty, (piece + 1) & 1u);
+            ga_commit(one, &sm.k_free[1]);                         // 2, 3 and 7
+            wait(&sm.dd_empty, 0u);
             tc_fence_after();
-            ga_pv<32, 544, kGaSCol>(one, d_v, 0u);
-            ga_commit(one, &sm.d_full);
-            ga_commit(one, &sm.k_free[1]);                         // 2, 3 and 8
-            ga_pv<160, 256, 256>(one, d_v, acc);
-            ga_commit(one, &sm.k_free[2]);                         // 4, 5 and 6
+            ga_pv<32, 544, kGaDCol>(one, d_v, 0u);
+            ga_commit(one, &sm.dd_full);
+            ga_pv<128, 256, 256>(one, d_v, acc);
+            ga_commit(one, &sm.k_free[2]);                         // 4, 5 and 8
             ga_commit(one, &sm.o_done);
-            piece += 3;
         }
     }
     // every MMA of this CTA is done before tensor memory goes back
@@ -802,8 +816,10 @@ group_attn_kernel(const GaArgs A) {
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.s_full, 1);
         mbar_init(&sm.p_full, kGaSoftWarps);
-        mbar_init(&sm.d_full, 1);
-        mbar_init(&sm.d_empty, kGaSoftWarps);
+        mbar_init(&sm.ds_full, 1);
+        mbar_init(&sm.ds_empty, kGaSoftWarps);
+        mbar_init(&sm.dd_full, 1);
+        mbar_init(&sm.dd_empty, kGaSoftWarps);
         mbar_init(&sm.o_done, 1);
         for (int i = 0; i < kGaRounds; ++i) {
             mbar_init(&sm.k_full[i], kGaDeqWarps);
