@@ -196,28 +196,28 @@ __device__ __forceinline__ void ga_commit(uint32_t one, uint64_t *bar) {
         ::"r"(smem_u32(bar)), "r"(one) : "memory");
 }
 
-// MMAs are issued by the lane whose `one` is set; the warp stays
-// together, so that the operands are uniform. A descriptor is its low word
-// (address and leading offset) plus a constant under a constant high word.
-template <int kD, uint32_t kIdesc, uint32_t kA, uint32_t kAHi, uint32_t kB, uint32_t kBHi>
-__device__ __forceinline__ void ga_mma_ss(uint32_t one, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate) {
+// MMAs are issued by the lane whose `one` is set; the warp stays together, so
+// that the operands are uniform. A descriptor is its low word (address and
+// leading offset) plus a constant under a constant high word.
+template <uint32_t kIdesc, uint32_t kA, uint32_t kAHi, uint32_t kB, uint32_t kBHi>
+__device__ __forceinline__ void ga_mma_ss(uint32_t one, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred e, p;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\t"
         "setp.ne.u32 e, %9, 0;\n\tsetp.ne.u32 p, %2, 0;\n\tadd.u32 a, %0, %5;\n\tadd.u32 b, %1, %7;\n\t"
         "mov.b64 da, {a, %6};\n\tmov.b64 db, {b, %8};\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%3], da, db, %4, p;\n\t}"
-        ::"r"(a_lo), "r"(b_lo), "r"(accumulate), "r"(kD), "n"(kIdesc), "n"(kA), "n"(kAHi), "n"(kB), "n"(kBHi), "r"(one)
+        ::"r"(a_lo), "r"(b_lo), "r"(accumulate), "r"(d), "n"(kIdesc), "n"(kA), "n"(kAHi), "n"(kB), "n"(kBHi), "r"(one)
         : "memory");
 }
 
 // A from tensor memory: lane = row, a 32-bit column holds two f16 of the K side.
-template <int kD, uint32_t kIdesc, int kACol, uint32_t kB, uint32_t kBHi>
-__device__ __forceinline__ void ga_mma_ts(uint32_t one, uint32_t b_lo, uint32_t accumulate) {
+template <uint32_t kIdesc, int kACol, uint32_t kB, uint32_t kBHi>
+__device__ __forceinline__ void ga_mma_ts(uint32_t one, uint32_t d, uint32_t b_lo, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred e, p;\n\t.reg .b32 b;\n\t.reg .b64 db;\n\t"
         "setp.ne.u32 e, %7, 0;\n\tsetp.ne.u32 p, %1, 0;\n\tadd.u32 b, %0, %5;\n\tmov.b64 db, {b, %6};\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%2], [%3], db, %4, p;\n\t}"
-        ::"r"(b_lo), "r"(accumulate), "r"(kD), "r"(kACol), "n"(kIdesc), "n"(kB), "n"(kBHi), "r"(one) : "memory");
+        ::"r"(b_lo), "r"(accumulate), "r"(d), "r"(kACol), "n"(kIdesc), "n"(kB), "n"(kBHi), "r"(one) : "memory");
 }
 
 // Words of a descriptor without swizzle (umma_desc).
@@ -274,20 +274,12 @@ __device__ __forceinline__ void ga_pair_bar(int id) { asm volatile("bar.sync %0,
 struct GaWait {
     bool dead = false;
     __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
-        if (mbar_try_wait(bar, parity) || dead) return;
-        for (int i = 0; i < 2000000; ++i)
+        for (int i = 0; i < (dead ? 1 : 2000000); ++i)
             if (mbar_try_wait_sleep(bar, parity, 1000u)) return;
         flag_status(kStatusTimeout);
         dead = true;
     }
 };
-
-// Two waits whose probes (100 cycles each) overlap.
-__device__ __forceinline__ void ga_wait2(GaWait &wait, uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb) {
-    const bool oa = mbar_try_wait(a, pa), ob = mbar_try_wait(b, pb);
-    if (!oa) wait(a, pa);
-    if (!ob) wait(b, pb);
-}
 
 // Two floats at once.
 __device__ __forceinline__ float2 ga_fma2(float2 a, float2 b, float2 c) {
@@ -708,33 +700,17 @@ __device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk w
     }
 }
 
-// Brings the pages of the blocks ahead to L2, at the pace of the first round.
-__device__ __forceinline__ void ga_prefetch(const GaArgs &A, GaSmem &sm, GaWalk walk, int lane) {
-    constexpr int kAhead = 4;
-    GaWait wait;
-    GaBlocks b = {walk, {}, 0, 0};
-    int n = 0;
-    for (bool more = b.segment(A); more; more = b.next(A), ++n) {
-        if (n >= kAhead) wait(&sm.k_free[0], (n - kAhead) & 1u);
-        const int page = b.take(A);
-        if (page < 0 || lane > 0) continue;
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
-                     ::"l"(A.kv_fp4 + static_cast<int64_t>(page) * (kPage * kFp4Bytes)), "r"(kPage * kFp4Bytes) : "memory");
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
-                     ::"l"(A.kv_scale + static_cast<int64_t>(page) * (kPage * kScaleBytes)), "r"(kPage * kScaleBytes) : "memory");
-    }
-}
-
 // The tensor memory address is 0: all of it is allocated. K-major operands:
 // leading offset along K (8 channels), stride offset along the rows; MN-major
 // (V): along the keys, along the channels.
-template <int kN, int kCh, int kCol>
-__device__ __forceinline__ void ga_pv(uint32_t one, uint32_t v_lo, uint32_t accumulate) {
-    constexpr uint32_t id = umma_idesc(kGaRows, kN, false, true), at = kCh / 8 * kGaKSlab >> 4, hi = ga_desc_hi(kGaKSlab);
-    ga_mma_ts<kCol, id, kGaPCol, at, hi>(one, v_lo, accumulate);
-    ga_mma_ts<kCol, id, kGaPCol + 8, at + 16, hi>(one, v_lo, 1u);
-    ga_mma_ts<kCol, id, kGaPCol + 16, at + 32, hi>(one, v_lo, 1u);
-    ga_mma_ts<kCol, id, kGaPCol + 24, at + 48, hi>(one, v_lo, 1u);
+// kN channels of V (at v_lo) into columns d, over the block's 64 keys.
+template <int kN>
+__device__ __forceinline__ void ga_pv(uint32_t one, uint32_t d, uint32_t v_lo, uint32_t accumulate) {
+    constexpr uint32_t id = umma_idesc(kGaRows, kN, false, true), hi = ga_desc_hi(kGaKSlab);
+    ga_mma_ts<id, kGaPCol, 0, hi>(one, d, v_lo, accumulate);
+    ga_mma_ts<id, kGaPCol + 8, 16, hi>(one, d, v_lo, 1u);
+    ga_mma_ts<id, kGaPCol + 16, 32, hi>(one, d, v_lo, 1u);
+    ga_mma_ts<id, kGaPCol + 24, 48, hi>(one, d, v_lo, 1u);
 }
 
 __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk) {
@@ -750,55 +726,40 @@ __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk)
         for (int kb = s.k0; kb < s.k1; ++kb, ++blk) {
             const uint32_t par = blk & 1u, acc = kb > s.k0;
             constexpr uint32_t id = umma_idesc(kGaRows, kGaBlk, false, false), hi = ga_desc_hi(128);
-            constexpr uint32_t da = 2 * kGaQSlab >> 4, db = 2 * kGaKSlab >> 4;          // 16 channels
-            // S's columns: the last piece there has been read
-            if (blk > 0) ga_wait2(wait, &sm.ds_empty, 1u, &sm.k_full[0], par);
-            else wait(&sm.k_full[0], par);
+            constexpr uint32_t da = 2 * kGaQSlab >> 4, db = 2 * kGaKSlab >> 4, dv = 8 * kGaKSlab >> 4;   // 16, 16 and 64 channels
+            wait(&sm.ds_empty, 1u);                                // S's columns: the last piece there has been read
+            tc_fence_after();
 #pragma unroll 1
             for (int r = 0; r < kGaRounds; ++r) {
-                if (r > 0) wait(&sm.k_full[r], par);
-                tc_fence_after();
-                const uint32_t a = d_q + r * (8 * da), b = d_k + r * (8 * db);
-                const uint32_t a3 = d_q + (6 + r) * (4 * da), b3 = d_k + (6 + r) * (4 * db);
-                ga_mma_ss<kGaSCol, id, 0, hi, 0, hi>(one, a, b, r > 0);
-                ga_mma_ss<kGaSCol, id, da, hi, db, hi>(one, a, b, 1u);
-                ga_mma_ss<kGaSCol, id, 2 * da, hi, 2 * db, hi>(one, a, b, 1u);
-                ga_mma_ss<kGaSCol, id, 3 * da, hi, 3 * db, hi>(one, a, b, 1u);
-                ga_mma_ss<kGaSCol, id, 4 * da, hi, 4 * db, hi>(one, a, b, 1u);
-                ga_mma_ss<kGaSCol, id, 5 * da, hi, 5 * db, hi>(one, a, b, 1u);
-                ga_mma_ss<kGaSCol, id, 6 * da, hi, 6 * db, hi>(one, a, b, 1u);
-                ga_mma_ss<kGaSCol, id, 7 * da, hi, 7 * db, hi>(one, a, b, 1u);
-                ga_mma_ss<kGaSCol, id, 0, hi, 0, hi>(one, a3, b3, 1u);
-                ga_mma_ss<kGaSCol, id, da, hi, db, hi>(one, a3, b3, 1u);
-                ga_mma_ss<kGaSCol, id, 2 * da, hi, 2 * db, hi>(one, a3, b3, 1u);
-                ga_mma_ss<kGaSCol, id, 3 * da, hi, 3 * db, hi>(one, a3, b3, 1u);
+                wait(&sm.k_full[r], par);
+#pragma unroll 1
+                for (int j = 0; j < 3; ++j) {
+                    const int c = j < 2 ? 2 * r + j : 6 + r;
+                    const uint32_t a = d_q + c * (4 * da), b = d_k + c * (4 * db);
+                    ga_mma_ss<id, 0, hi, 0, hi>(one, kGaSCol, a, b, r + j > 0);
+                    ga_mma_ss<id, da, hi, db, hi>(one, kGaSCol, a, b, 1u);
+                    ga_mma_ss<id, 2 * da, hi, 2 * db, hi>(one, kGaSCol, a, b, 1u);
+                    ga_mma_ss<id, 3 * da, hi, 3 * db, hi>(one, kGaSCol, a, b, 1u);
+                }
             }
             ga_commit(one, &sm.s_full);
             wait(&sm.p_full, par);
             tc_fence_after();
             // O in parts of 128 channels between the pieces (64 columns of S's and 32 of their own, twice), so that
             // 400 cycles of other MMAs lie between a piece and the next use of its columns
-            ga_pv<64, 384, kGaSCol>(one, d_v, 0u);
-            ga_commit(one, &sm.ds_full);
-            if (blk > 0) {
-                wait(&sm.dd_empty, 1u);
+#pragma unroll 1
+            for (uint32_t h = 0; h < 2; ++h) {
+                if (h > 0) wait(&sm.ds_empty, 0u);
+                ga_pv<64>(one, kGaSCol, d_v + 6 * dv + h * (3 * dv / 2), 0u);
+                ga_commit(one, &sm.ds_full);
+                wait(&sm.dd_empty, h ^ 1u);
                 tc_fence_after();
+                ga_pv<32>(one, kGaDCol, d_v + 7 * dv + h * (3 * dv / 2), 0u);
+                ga_commit(one, &sm.dd_full);
+                ga_pv<128>(one, 128 * h, d_v + h * (2 * dv), acc);
+                ga_commit(one, &sm.k_free[h]);                     // chunks 2 h, 2 h + 1 and 6 + h
             }
-            ga_pv<32, 448, kGaDCol>(one, d_v, 0u);
-            ga_commit(one, &sm.dd_full);
-            ga_pv<128, 0, 0>(one, d_v, acc);
-            ga_commit(one, &sm.k_free[0]);                         // chunks 0, 1 and 6
-            wait(&sm.ds_empty, 0u);
-            tc_fence_after();
-            ga_pv<64, 480, kGaSCol>(one, d_v, 0u);
-            ga_commit(one, &sm.ds_full);
-            ga_pv<128, 128, 128>(one, d_v, acc);
-            ga_commit(one, &sm.k_free[1]);                         // 2, 3 and 7
-            wait(&sm.dd_empty, 0u);
-            tc_fence_after();
-            ga_pv<32, 544, kGaDCol>(one, d_v, 0u);
-            ga_commit(one, &sm.dd_full);
-            ga_pv<128, 256, 256>(one, d_v, acc);
+            ga_pv<128>(one, 256, d_v + 4 * dv, acc);
             ga_commit(one, &sm.k_free[2]);                         // 4, 5 and 8
             ga_commit(one, &sm.o_done);
         }
@@ -870,8 +831,6 @@ group_attn_kernel(const GaArgs A) {
             ga_mma(A, sm, walk);
         else if (warp < kGaDeqWarp + kGaDeqWarps)
             ga_dequant(A, sm, walk, warp - kGaDeqWarp, lane);
-        else
-            ga_prefetch(A, sm, walk, lane);
     }
     __syncwarp();
     tc_fence_before();
