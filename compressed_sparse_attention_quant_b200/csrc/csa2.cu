@@ -699,7 +699,7 @@ csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D, const csa2_
     const int ctas = std::min(dev->sm_count, kGaMaxCtas);
     cudaError_t e = launch_pdl(group_attn_kernel, dim3(ctas), dim3(kGaThreads), kGaSmemBytes, st, A);
     if (e != cudaSuccess) return CSA2_ERR_CUDA;
-    return cuda_status(launch_pdl(group_attn_merge_kernel, dim3(4 * ctas), dim3(kGmThreads), 0, st, A));
+    return cuda_status(launch_pdl(group_attn_merge_kernel, dim3(kGmCtasPerSm * ctas), dim3(kGmThreads), 0, st, A));
 }
 
 csa2_status csa2_plan(const int *modes, int n_layers, int *kv_owner, int *index_src) {

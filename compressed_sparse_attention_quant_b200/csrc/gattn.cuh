@@ -67,7 +67,7 @@ constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a 
 // A block's nine chunks are filled, multiplied and released in three rounds, in
 // the order in which O's MMAs are done with them: 2 r, 2 r + 1 and 6 + r.
 constexpr int kGaRounds = 3;
-constexpr int kGaGap = 2;                                          // steps a row tile counts for beside its blocks
+constexpr int kGaGap = 5;                                          // steps a row tile counts for beside its blocks
 constexpr float kGaSlack = 8.0f;                                   // log2 units a block may exceed the reference
 static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 96, "tensor memory is full; pieces of 64, 32, 64 and 32 channels");
 
@@ -85,7 +85,7 @@ struct GaArgs {
     __nv_bfloat16 *out;                // [N][16][576]
     float *lse;                        // [N][16]
     struct GaPlan *plan;
-    float *part_o;                     // [2 * ranges][tok_slots][576][16]
+    float *part_o;                     // [2 * ranges][tok_slots][144][16][4]: 4 channels of 16 heads together
     float2 *part_ml;                   // [2 * ranges][tok_slots * 16]: (m in the log2 domain, l)
     int tok_slots;                     // min(8, N)
 };
@@ -98,7 +98,8 @@ struct GaPlan {
     struct Tile { int64_t begin; int blocks, tok0, ntok; } first[kGaMaxCtas];
 };
 
-__host__ __device__ __forceinline__ int64_t ga_range(int64_t total, int c, int ranges) { return total * c / ranges; }
+// First step of range c.
+__device__ __forceinline__ int64_t ga_range(int64_t total, int c, int ranges) { return total * c / ranges; }
 
 struct GaGroup { int tok0, n, T, blocks; };
 
@@ -353,8 +354,10 @@ __device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaS
         const int h = half * 8 + (lane & 7), row = warp * kHeads + h, part = lane >> 3;
         const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (static_cast<int64_t>(s.tok0 + (some ? warp : 0)) * kHeads + h) * kDim) + part;
         uint8_t *dst = sm.q + part * kGaQSlab + row * 16;
-        float mx = 0.0f, down = sign;
+        float mx, down = sign;
+#pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
+            uint32_t m2 = 0u;                                      // bf16 magnitudes order as integers
 #pragma unroll 1
             for (int u0 = 0; u0 < 18; u0 += 9) {
                 uint4 v[9];
@@ -365,16 +368,18 @@ __device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaS
                     uint32_t o[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 f = bf16x2_f32((&v[u].x)[e]);
-                        mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        const uint32_t w = (&v[u].x)[e];
+                        m2 = __vmaxu2(m2, w & 0x7fff7fffu);
+                        const float2 f = bf16x2_f32(w);
                         o[e] = f32x2_f16x2(f.x * down, f.y * down);
                     }
                     *reinterpret_cast<uint4 *>(dst + 4 * (u0 + u) * kGaQSlab) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
+            mx = __uint_as_float(max(m2 & 0xffff0000u, m2 << 16));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const int eq = f16_exponent(mx);
+            const int eq = mx < INFINITY ? f16_exponent(mx) : 0;   // a row with inf or NaN stays one
             // never 0: entries that do not count have a score of -inf, which has to stay one
             if (part == 0) sm.scale[row] = fmaxf(fabsf(A.scale_log2) * exp2f(static_cast<float>(eq)), 1e-30f);
             if (!__any_sync(0xffffffffu, eq != 0)) break;
@@ -552,24 +557,25 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
         ga_pair_bar(pair_bar);
         l = sm.l[row];
         if (s.k0 > 0 || s.k1 < s.blocks) {
-            // part of a row tile: unnormalised, [slot][token][channel][head]
+            // part of a row tile: unnormalised, 4 channels of a head together. The sums in
+            // registers leave in pairs: as fours they would cost spilled registers.
             const int64_t slot = 2 * blockIdx.x + (seg_no > 0);
-            float *po = A.part_o + (slot * A.tok_slots + tok) * (kDim * kHeads) + h;
+            float2 *po = reinterpret_cast<float2 *>(A.part_o) + (slot * A.tok_slots + tok) * (kDim * kHeads / 2) + 2 * h;
             if (live && half == 0) A.part_ml[(slot * A.tok_slots + tok) * kHeads + h] = make_float2(m, l);
 #pragma unroll 1
             for (int c = 0; c < kGaTmemCh / 2; c += 16) {
                 float a[16];
                 tmem_ld16(tm + half * (kGaTmemCh / 2) + c, a);
+                float2 *to = po + (half * (kGaTmemCh / 2) + c) / 4 * (2 * kHeads);
                 if (live)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) po[(half * (kGaTmemCh / 2) + c + i) * kHeads] = a[i];
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<float4 *>(to + i * (2 * kHeads)) = make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
             }
             if (live)
 #pragma unroll
-                for (int i = 0; i < kGaRegs / 2; ++i) {
-                    po[(ga_reg_channel(2 * i & ~15, half) + (2 * i & 15)) * kHeads] = acc[i].x;
-                    po[(ga_reg_channel(2 * i & ~15, half) + (2 * i & 15) + 1) * kHeads] = acc[i].y;
-                }
+                for (int i = 0; i < kGaRegs / 2; ++i)
+                    po[(ga_reg_channel(2 * i & ~15, half) + (2 * i & 15)) / 4 * (2 * kHeads) + (i & 1)] = acc[i];
         } else {
             // the whole row tile: join the token's own part and write it
             const int64_t r = static_cast<int64_t>(s.tok0 + (live ? tok : 0)) * kHeads + h;
@@ -846,155 +852,139 @@ group_attn_kernel(const GaArgs A) {
 // Joins the partials of the row tiles that K12's ranges cut, with the own
 // part. Memory-bound in principle (36,864 B per partial and token, L2), latency
 // bound per unit of work, so a unit is one slice of a token's channels: all
-// 576, 64 or 16 of them, the smaller the fewer tokens there are to fill the
-// GPU. A thread takes 4 heads of a channel; with 16 channels the four groups of
-// 64 threads take every fourth partial each.
+// 192, 64 or 16 of them, the smaller the fewer tokens there are to fill the
+// GPU, and the first partials are loaded together with the maxima and sums. A
+// thread takes 4 channels of a head; with 16 channels the four groups of 64
+// threads take every fourth partial each.
 constexpr int kGmThreads = 256;
+constexpr int kGmCtasPerSm = 4;
+constexpr int kGmBatch = 8;                                        // partials loaded together
 
 struct GmSmem {
-    float w[kGaMaxCtas + 1][kHeads];                               // weight of a partial
-    float red[kGmThreads / kHeads][kHeads];
-    union {
-        float4 sum[4][64];
-        alignas(16) uint16_t out[kHeads][kDim + 8];
-    };
-    float inv[kHeads], fo[kHeads];
-    int first[kGaMaxCtas + 1];                                     // units before the c-th boundary's tile
+    GaPlan::Tile first[kGaMaxCtas];
+    alignas(16) float2 ml[kGaMaxCtas + 1][kHeads];                 // (m, l) of a partial, then (its weight, -)
+    float red[2][kGmThreads / kHeads][kHeads];
+    float4 sum[4][64];
+    int before[kGaMaxCtas + 1];                                    // tokens up to a boundary
     int warp_sum[kGmThreads / 32];
 };
 
-// The token's weights: of partial p for head h in sm.w, of the own part in sm.fo.
-struct GmTile {
-    int n, slot0, c0;                                              // partials; the first one's slot; its range
-    __device__ __forceinline__ int slot(int p) const { return p == 0 ? slot0 : 2 * (c0 + p); }
-};
-
-__device__ __forceinline__ void gm_weights(const GaArgs &A, GmSmem &sm, const GmTile &t, int tok, int64_t row, bool first) {
-    const int tid = threadIdx.x, h = tid & (kHeads - 1), at = tid >> 4;
-    constexpr int kLanes = kGmThreads / kHeads, kMost = (kGaMaxCtas + kLanes) / kLanes;
-    float2 ml[kMost];
-    float own = -INFINITY;
-    if (A.lse_own) own = __ldg(A.lse_own + row + h) * 1.4426950408889634f;
-    float mx = own;
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-        const int p = at + i * kLanes;
-        ml[i] = make_float2(-INFINITY, 0.0f);
-        if (p < t.n) ml[i] = __ldcg(&A.part_ml[(static_cast<int64_t>(t.slot(p)) * A.tok_slots + tok) * kHeads + h]);
-    }
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) mx = fmaxf(mx, ml[i].x);
-    sm.red[at][h] = mx;
-    __syncthreads();
-    for (int i = 0; i < kLanes; ++i) mx = fmaxf(mx, sm.red[i][h]);
-    const float ref = mx == -INFINITY ? 0.0f : mx;
-    __syncthreads();
-    float l = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-        const int p = at + i * kLanes;
-        if (p < t.n) {
-            const float w = ga_ex2(ml[i].x - ref);
-            sm.w[p][h] = w;
-            l += ml[i].y * w;
-        }
-    }
-    sm.red[at][h] = l;
-    __syncthreads();
-    if (tid < kHeads) {
-        const float wo = ga_ex2(own - ref);
-        l = wo;
-        for (int i = 0; i < kLanes; ++i) l += sm.red[i][h];
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;             // a NaN stays one
-        sm.inv[h] = inv;
-        sm.fo[h] = wo > 0.0f ? wo * inv : 0.0f;                    // nothing to read without an own part
-        if (first) A.lse[row + h] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
-    }
-    __syncthreads();
-}
-
-// kPer x 64 channels of a token from col0 on.
+// kPer x 64 channels of a token from col0 on, or (kPer = 0) 16 channels.
 template <int kPer>
-__device__ __forceinline__ void gm_slice(const GaArgs &A, GmSmem &sm, const GmTile &t, int tok, int64_t row, int col0) {
-    const int tid = threadIdx.x, hq = (tid & 3) * 4, col = col0 + (tid >> 2);
-    float4 a[kPer];
+__device__ __forceinline__ void gm_slice(const GaArgs &A, GmSmem &sm, int c0, int n, int slot0, int tok, int64_t row,
+                                         int col0, bool write_lse) {
+    constexpr int kGroups = kPer == 0 ? 4 : 1, kV = kPer == 0 ? 1 : kPer, kAtOnce = kPer == 3 ? 2 : kGmBatch;
+    const int tid = threadIdx.x, h = tid & (kHeads - 1), at = tid >> 4;
+    const int grp = kPer == 0 ? tid >> 6 : 0, c4 = col0 / 4 + (kPer == 0 ? (tid & 63) >> 4 : at);
+    const float4 *po = reinterpret_cast<const float4 *>(A.part_o) + static_cast<int64_t>(tok) * (kDim * kHeads / 4) + c4 * kHeads + h;
+    auto slot = [&](int p) { return static_cast<int64_t>(p == 0 ? slot0 : 2 * (c0 + p)) * A.tok_slots; };
+    float4 v[kAtOnce][kV];
+    auto load = [&](int b) {                                       // partials b, b + kGroups, ..
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) a[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll (kPer == 1 ? 8 : 1)
-    for (int p = 0; p < t.n; ++p) {
-        const float4 *src = reinterpret_cast<const float4 *>(
-            A.part_o + ((static_cast<int64_t>(t.slot(p)) * A.tok_slots + tok) * kDim + col) * kHeads + hq);
-        const float4 w = *reinterpret_cast<const float4 *>(&sm.w[p][hq]);
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int p = min(b + i * kGroups, n - 1);             // past the end: the last one again, weight 0
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const float4 v = __ldcg(src + i * (64 * kHeads / 4));
-            a[i].x += w.x * v.x;
-            a[i].y += w.y * v.y;
-            a[i].z += w.z * v.z;
-            a[i].w += w.w * v.w;
+            for (int k = 0; k < kV; ++k) v[i][k] = __ldcg(po + slot(p) * (kDim * kHeads / 4) + k * (16 * kHeads));
         }
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int h = hq + e, c = col + 64 * i;
-            float v = (&a[i].x)[e] * sm.inv[h];
-            if (sm.fo[h] != 0.0f) v += sm.fo[h] * __ldg(A.o_own + (row + h) * kDim + c);
-            const __nv_bfloat16 b = __float2bfloat16_rn(v);
-            sm.out[h][c - col0] = *reinterpret_cast<const uint16_t *>(&b);
-        }
+    };
+    constexpr int kLanes = kGmThreads / kHeads;
+    for (int p = at; p < n; p += kLanes)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;"
+                     ::"r"(smem_u32(&sm.ml[p][h])), "l"(&A.part_ml[(slot(p) + tok) * kHeads + h]) : "memory");
+    cp_async_commit();
+    load(grp);
+    // ---- weights
+    const float own = A.lse_own ? __ldg(A.lse_own + row + h) * 1.4426950408889634f : -INFINITY;
+    float mx = own;
+    cp_async_wait<0>();
+    for (int p = at; p < n; p += kLanes) mx = fmaxf(mx, sm.ml[p][h].x);
+    sm.red[0][at][h] = mx;
     __syncthreads();
-    for (int i = tid; i < kHeads * kPer * 8; i += kGmThreads) {    // 8 channels each
-        const int h = i / (kPer * 8), c = i % (kPer * 8) * 8;
-        *reinterpret_cast<uint4 *>(A.out + (row + h) * kDim + col0 + c) = *reinterpret_cast<const uint4 *>(&sm.out[h][c]);
+#pragma unroll
+    for (int i = 0; i < kLanes; ++i) mx = fmaxf(mx, sm.red[0][i][h]);
+    const float ref = mx == -INFINITY ? 0.0f : mx;
+    float l = 0.0f;
+    for (int p = at; p < n; p += kLanes) {
+        const float w = ga_ex2(sm.ml[p][h].x - ref);
+        l += sm.ml[p][h].y * w;
+        sm.ml[p][h].x = w;
     }
+    sm.red[1][at][h] = l;
+    __syncthreads();
+    const float wo = ga_ex2(own - ref);
+    l = wo;
+#pragma unroll
+    for (int i = 0; i < kLanes; ++i) l += sm.red[1][i][h];
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;                 // a NaN stays one
+    const float fo = wo > 0.0f ? wo * inv : 0.0f;                  // nothing to read without an own part
+    if (write_lse && at == 0) A.lse[row + h] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+    // ---- the channels
+    float4 a[kV];
+#pragma unroll
+    for (int k = 0; k < kV; ++k) a[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int b = grp; b < n; b += kAtOnce * kGroups) {
+        if (b != grp) load(b);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int p = b + i * kGroups;
+            const float w = p < n ? sm.ml[p][h].x : 0.0f;
+#pragma unroll
+            for (int k = 0; k < kV; ++k) {
+                a[k].x += w * v[i][k].x;
+                a[k].y += w * v[i][k].y;
+                a[k].z += w * v[i][k].z;
+                a[k].w += w * v[i][k].w;
+            }
+        }
+    }
+    if constexpr (kPer == 0) {
+        sm.sum[grp][tid & 63] = a[0];
+        __syncthreads();
+        if (grp == 0)
+#pragma unroll
+            for (int i = 1; i < 4; ++i) {
+                const float4 o = sm.sum[i][tid];
+                a[0].x += o.x;
+                a[0].y += o.y;
+                a[0].z += o.z;
+                a[0].w += o.w;
+            }
+    }
+    if (grp == 0)
+#pragma unroll
+        for (int k = 0; k < kV; ++k) {
+            const int64_t to = (row + h) * kDim + (c4 + 16 * k) * 4;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (fo != 0.0f) o = __ldg(reinterpret_cast<const float4 *>(A.o_own + to));
+            const __nv_bfloat162 x = __floats2bfloat162_rn(a[k].x * inv + fo * o.x, a[k].y * inv + fo * o.y);
+            const __nv_bfloat162 y = __floats2bfloat162_rn(a[k].z * inv + fo * o.z, a[k].w * inv + fo * o.w);
+            *reinterpret_cast<uint2 *>(A.out + to) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+        }
     __syncthreads();
 }
 
-// 16 channels of a token from col0 on.
-__device__ __forceinline__ void gm_slice16(const GaArgs &A, GmSmem &sm, const GmTile &t, int tok, int64_t row, int col0) {
-    const int tid = threadIdx.x, grp = tid >> 6, col = (tid & 63) >> 2, hq = (tid & 3) * 4;
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (int p = grp; p < t.n; p += 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-            A.part_o + ((static_cast<int64_t>(t.slot(p)) * A.tok_slots + tok) * kDim + col0 + col) * kHeads + hq));
-        const float4 w = *reinterpret_cast<const float4 *>(&sm.w[p][hq]);
-        a.x += w.x * v.x;
-        a.y += w.y * v.y;
-        a.z += w.z * v.z;
-        a.w += w.w * v.w;
-    }
-    sm.sum[grp][tid & 63] = a;
-    __syncthreads();
-    const int h = tid >> 4, c = tid & 15;                          // one output per thread
-    float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v += reinterpret_cast<const float *>(&sm.sum[i][c * 4 + (h >> 2)])[h & 3];
-    const int64_t at = (row + h) * kDim + col0 + c;
-    v *= sm.inv[h];
-    if (sm.fo[h] != 0.0f) v += sm.fo[h] * __ldg(A.o_own + at);
-    A.out[at] = __float2bfloat16_rn(v);
-    __syncthreads();
-}
-
-__global__ void __launch_bounds__(kGmThreads, 4)
+__global__ void __launch_bounds__(kGmThreads, kGmCtasPerSm)
 group_attn_merge_kernel(const GaArgs A) {
     __shared__ GmSmem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_trigger();
-    const int64_t total = A.plan->total;
-    const int ranges = A.plan->ranges;
+    const int64_t total = __ldcg(&A.plan->total);
+    const int ranges = __ldcg(&A.plan->ranges);
+    GaPlan::Tile mine = {};
+    if (tid < kGaMaxCtas) {                                        // beyond the ranges: whatever is there, not looked at
+        mine.begin = __ldcg(&A.plan->first[tid].begin);
+        mine.blocks = __ldcg(&A.plan->first[tid].blocks);
+        mine.tok0 = __ldcg(&A.plan->first[tid].tok0);
+        mine.ntok = __ldcg(&A.plan->first[tid].ntok);
+        sm.first[tid] = mine;
+    }
     // The range boundary c cuts the row tile of range c's first step when the
     // tile begins before it; the first such boundary of a tile stands for it.
-    int mine = 0;
-    if (tid > 0 && tid < ranges) {
-        const GaPlan::Tile &t = A.plan->first[tid];
-        if (t.begin < ga_range(total, tid, ranges) && t.begin >= ga_range(total, tid - 1, ranges)) mine = t.ntok;
-    }
-    int incl = mine;
+    int incl = 0;
+    if (tid > 0 && tid < ranges && mine.begin < ga_range(total, tid, ranges) && mine.begin >= ga_range(total, tid - 1, ranges))
+        incl = mine.ntok;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, incl, d);
@@ -1003,32 +993,30 @@ group_attn_merge_kernel(const GaArgs A) {
     if (lane == 31) sm.warp_sum[warp] = incl;
     __syncthreads();
     for (int w = 0; w < warp; ++w) incl += sm.warp_sum[w];
-    if (tid < kGaMaxCtas) sm.first[tid + 1] = incl;                // tokens up to boundary tid
-    if (tid == 0) sm.first[0] = 0;
+    if (tid < kGaMaxCtas) sm.before[tid + 1] = incl;
+    if (tid == 0) sm.before[0] = 0;
     __syncthreads();
-    const int tokens = sm.first[kGaMaxCtas];
-    // slices of 16 channels while 36 of them per token fit one wave of CTAs, then of 64, then whole tokens
+    const int tokens = sm.before[kGaMaxCtas];
+    // slices of 16 channels while 36 of them per token fit one wave of CTAs, then of 64, then of 192
     const int grid = static_cast<int>(gridDim.x);
-    const int per = tokens * 36 <= grid ? 36 : tokens * 9 <= 2 * grid ? 9 : 1;
+    const int per = tokens * 36 <= grid ? 36 : tokens * 9 <= 2 * grid ? 9 : 3;
     for (int unit = blockIdx.x; unit < tokens * per; unit += grid) {
         const int ut = unit / per, slice = unit - ut * per;
-        int lo = 0, hi = kGaMaxCtas;                               // the boundary: first[c] <= ut < first[c + 1]
+        int lo = 0, hi = kGaMaxCtas;                               // the boundary: before[c] <= ut < before[c + 1]
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (sm.first[mid] <= ut) lo = mid; else hi = mid;
+            if (sm.before[mid] <= ut) lo = mid; else hi = mid;
         }
-        const GaPlan::Tile tile = A.plan->first[lo];
-        const int tok = ut - sm.first[lo];
-        // ranges lo - 1 (which begins the tile) to the last c with total * c / ranges < the tile's end
-        GmTile t;
-        t.c0 = lo - 1;
-        t.n = static_cast<int>(((tile.begin + tile.blocks) * ranges - 1) / total) - t.c0 + 1;
-        t.slot0 = 2 * t.c0 + (ga_range(total, t.c0, ranges) < tile.begin - kGaGap ? 1 : 0);   // a range's first tile: slot 0
-        const int64_t row = static_cast<int64_t>(tile.tok0 + tok) * kHeads;
-        gm_weights(A, sm, t, tok, row, slice == 0);
-        if (per == 36) gm_slice16(A, sm, t, tok, row, slice * 16);
-        else if (per == 9) gm_slice<1>(A, sm, t, tok, row, slice * 64);
-        else gm_slice<9>(A, sm, t, tok, row, 0);
+        const GaPlan::Tile &t = sm.first[lo];
+        const int tok = ut - sm.before[lo];
+        // ranges c0 = lo - 1 (which begins the tile) to the last c with total * c / ranges < the tile's end; a range's
+        // first tile is in its slot 0
+        const int c0 = lo - 1, n = static_cast<int>(((t.begin + t.blocks) * ranges - 1) / total) - c0 + 1;
+        const int slot0 = 2 * c0 + (ga_range(total, c0, ranges) < t.begin - kGaGap ? 1 : 0);
+        const int64_t row = static_cast<int64_t>(t.tok0 + tok) * kHeads;
+        if (per == 36) gm_slice<0>(A, sm, c0, n, slot0, tok, row, slice * 16, slice == 0);
+        else if (per == 9) gm_slice<1>(A, sm, c0, n, slot0, tok, row, slice * 64, slice == 0);
+        else gm_slice<3>(A, sm, c0, n, slot0, tok, row, slice * 192, slice == 0);
     }
 }
 
