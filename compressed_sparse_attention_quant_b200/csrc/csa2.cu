@@ -93,7 +93,8 @@ cudaError_t device_info(DeviceInfo **out) {
                                  reinterpret_cast<const void *>(lse_merge_kernel),
                                  reinterpret_cast<const void *>(swa_replay_kernel),
                                  reinterpret_cast<const void *>(append_kv_rope_kernel),
-                                 reinterpret_cast<const void *>(rope_rows_kernel),
+                                 reinterpret_cast<const void *>(rope_rows_kernel<true>),
+                                 reinterpret_cast<const void *>(rope_rows_kernel<false>),
                                  reinterpret_cast<const void *>(group_attn_kernel),
                                  reinterpret_cast<const void *>(group_attn_merge_kernel)};
         for (const void *kf : kernels) {
@@ -617,7 +618,7 @@ csa2_status csa2_append_kv_rope(const void *x_bf16, int64_t x_stride, int64_t n_
     A.kidx = static_cast<uint8_t *>(cache->kidx);
     A.kidx_scale = cache->kidx_scale;
     A.n_slots = cache->num_pages * kPage;
-    return cuda_status(launch_append_kv_rope(A, static_cast<cudaStream_t>(stream)));
+    return cuda_status(launch_append_kv_rope(A, dev->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 csa2_status csa2_rope_rows(const void *x_bf16, int64_t x_stride, int64_t n_tok, int heads, int dim,
@@ -647,7 +648,7 @@ csa2_status csa2_rope_rows(const void *x_bf16, int64_t x_stride, int64_t n_tok, 
     A.dim = dim;
     A.pos = positions;
     A.rope = rope_args(rope);
-    return cuda_status(launch_rope_rows(A, static_cast<cudaStream_t>(stream)));
+    return cuda_status(launch_rope_rows(A, dev->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 size_t csa2_group_attn_workspace_bytes(int N, int G) {

@@ -161,10 +161,11 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
     return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
 }
 
-// One row's quantisation, shared by four neighbouring lanes (gmask): this
+// One row's quantisation, shared by four neighbouring lanes (every lane of mask
+// takes part, with its own row): this
 // lane's 16 channels as bf16 pairs w (channels 8t .. 8t + 7, then
 // 32 + 8t .. 32 + 8t + 7) become the packed codes o; every lane gets sigma.
-__device__ __forceinline__ void fp8_row_codes(const uint32_t (&w)[8], unsigned gmask, float &sg, uint32_t (&o)[4]) {
+__device__ __forceinline__ void fp8_row_codes(const uint32_t (&w)[8], unsigned mask, float &sg, uint32_t (&o)[4]) {
     float f[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -174,8 +175,8 @@ __device__ __forceinline__ void fp8_row_codes(const uint32_t (&w)[8], unsigned g
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
-    amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, 2));
+    amax = fmaxf(amax, __shfl_xor_sync(mask, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(mask, amax, 2));
     // sigma = RN(amax / 448): one rounded product and one fma
     // correction (equal to the IEEE quotient for every finite bf16
     // amax, checked exhaustively on the host).
@@ -203,7 +204,7 @@ __device__ __forceinline__ void fp8_row_codes(const uint32_t (&w)[8], unsigned g
         mag[i] = lo;
         near |= lo != hi ? (1u << i) : 0u;
     }
-    if (__any_sync(gmask, near != 0u)) {                // rare: exact fix-up of close calls
+    if (__any_sync(mask, near != 0u)) {                // rare: exact fix-up of close calls
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (near & (1u << i)) {
@@ -229,8 +230,7 @@ quant_index_fp8_kernel(const uint4 *__restrict__ x, int64_t n_rows, uint2 *__res
                        float *__restrict__ sigma) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, part = threadIdx.x & (kIdxQuantTpr - 1);
-    const unsigned gmask = 0xfu << (lane & 28);         // the 4 lanes of this row
+    const int part = threadIdx.x & (kIdxQuantTpr - 1);
     // Each thread keeps its next kIdxQuantStages rows in flight with cp.async
     // into its own shared-memory slots (no registers held, no barrier: a
     // thread reads only what it copied).
@@ -250,7 +250,8 @@ quant_index_fp8_kernel(const uint4 *__restrict__ x, int64_t n_rows, uint2 *__res
         fetch(k);
         cp_async_commit();
     }
-    for (int64_t k = 0; row0 + k * stride < n_rows; ++k) {
+    // all lanes of a warp go on while its first row is there: they shuffle together
+    for (int64_t k = 0; row0 - (threadIdx.x & 31) / kIdxQuantTpr + k * stride < n_rows; ++k) {
         fetch(k + kIdxQuantStages - 1);
         cp_async_commit();
         cp_async_wait<kIdxQuantStages - 1>();           // row k has landed
@@ -261,7 +262,7 @@ quant_index_fp8_kernel(const uint4 *__restrict__ x, int64_t n_rows, uint2 *__res
             const uint32_t w[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
             float sg;
             uint32_t o[4];
-            fp8_row_codes(w, gmask, sg, o);
+            fp8_row_codes(w, 0xffffffffu, sg, o);
             if (row < n_rows) {
                 codes[row * 8 + part] = make_uint2(o[0], o[1]);           // channels 8t .. 8t + 7
                 codes[row * 8 + 4 + part] = make_uint2(o[2], o[3]);       // channels 32 + 8t ..

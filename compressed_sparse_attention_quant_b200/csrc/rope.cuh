@@ -15,8 +15,6 @@
 // bytes of rotating first and quantising after.
 #pragma once
 
-#include <cuda_fp4.h>
-
 #include "common.cuh"
 #include "quant.cuh"
 
@@ -52,19 +50,22 @@ struct RopeArgs {
 };
 
 // ------------------------------------------------------------------ K10
-// One CTA takes 8 tokens: 36 threads per token, one per 16-channel group, and
-// one more warp whose 4 lanes per token take the indexer key. The rotated
-// channels go through shared memory first (pair by pair, all threads), because
-// a pair may lie in two groups and its angle serves the indexer key as well
-// when both rows are rotated by the same frequencies.
-constexpr int kApTok = 8;
-constexpr int kApGroups = kDim / kGroup;                          // 36
-constexpr int kApLatent = kApTok * kApGroups;                     // 288
-constexpr int kApThreads = kApLatent + kApTok * 4;                // 320
+// A warp takes up to 4 tokens by itself, without a barrier: all their rows are
+// on the way while it computes the angles. Rotated channels go through shared
+// memory (a token at a time, a lane per pair), because a pair may lie in two
+// groups and its angle serves the indexer key as well when both rows are
+// rotated by the same frequencies. Then a lane quantises one 16-channel group
+// of each token, and of the last step, with four groups and the key of every
+// token left, 16 lanes take the groups and 16 the keys, 4 lanes per key.
+constexpr int kApTok = 4;
+constexpr int kApWarps = 4;
+constexpr int kApThreads = 32 * kApWarps;
+constexpr int kApCtasPerSm = 5;
 
 struct AppendArgs {
     const uint16_t *x;                 // [n][x_stride] bf16
     int64_t x_stride, n;
+    int tokens;                        // per warp, 1 .. kApTok
     const int32_t *pos, *slots;
     RopeArgs rope;
     const uint16_t *k;                 // [n][k_stride] bf16, or null
@@ -76,22 +77,36 @@ struct AppendArgs {
     int64_t n_slots;
 };
 
-// Rounds a positive value to 12 significant bits. A bf16 magnitude over an
-// E4M3 scale, and a sixth of one, either equals a rounding midpoint of the
-// code or lies at least 2^-8 of it away (both sides are integers of at most 8
-// bits up to a power of two). So after this step a quotient taken with an
-// approximate reciprocal (2^-22) sits exactly on its midpoint or on its right
-// side, and the conversion's round-to-nearest-even decides as it would for the
-// exact quotient.
+// Rounds a positive value to 12 significant bits. A sixth of a bf16 magnitude
+// either equals a rounding midpoint of E4M3 or lies at least 2^-8 of it away
+// (both sides are integers of at most 8 bits up to a power of two). So after
+// this step the product with the rounded 1/6 sits exactly on its midpoint or on
+// its right side, and the conversion's round-to-nearest-even decides as it
+// would for the exact quotient.
 __device__ __forceinline__ float snap12(float v) {
     return __uint_as_float((__float_as_uint(v) + 0x800u) & 0xfffff000u);
 }
 
+// The same for the quotients x / s, with an approximate reciprocal (2^-22) and
+// a grid of 2^-13: E2M1's midpoints are multiples of 1/4, any other quotient is
+// at least 2^-10 away from them, and one so large that the grid is coarser is
+// far above 6, where the codes end.
+__device__ __forceinline__ float2 snap_quotients(float2 x, float r) {
+    constexpr float kGrid = 1536.0f;                              // binary32 values around it lie 2^-13 apart
+    float2 v;
+    asm("{.reg .b64 x, r, c, n, v;\n\t"
+        "mov.b64 x, {%2, %3}; mov.b64 r, {%4, %4}; mov.b64 c, {%5, %5}; mov.b64 n, {%6, %6};\n\t"
+        "fma.rn.f32x2 v, x, r, c; add.rn.f32x2 v, v, n;\n\t"
+        "mov.b64 {%0, %1}, v;}"
+        : "=f"(v.x), "=f"(v.y) : "f"(x.x), "f"(x.y), "f"(r), "f"(kGrid), "f"(-kGrid));
+    return v;
+}
+
 // 16 bf16 channels (8 pairs) -> 8 bytes of E2M1 codes and the E4M3 scale byte.
 __device__ __forceinline__ uint2 fp4_group(const uint32_t (&w)[8], uint32_t &scale_byte) {
-    uint32_t m = 0u;
+    uint32_t m = w[0] & 0x7fff7fffu;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    for (int i = 1; i < 8; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
     const float amax = __uint_as_float(max(m & 0xffff0000u, m << 16));
     scale_byte = static_cast<uint32_t>(__nv_cvt_float_to_fp8(snap12(amax * (1.0f / 6.0f)), __NV_SATFINITE, __NV_E4M3));
     const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(scale_byte), __NV_E4M3)));
@@ -99,13 +114,16 @@ __device__ __forceinline__ uint2 fp4_group(const uint32_t (&w)[8], uint32_t &sca
     uint32_t packed[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        uint32_t c = 0u;
+        float2 q[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t v = w[4 * h + i];
-            const float a = snap12(__uint_as_float(v << 16) * r), b = snap12(__uint_as_float(v & 0xffff0000u) * r);
-            c |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(a, b), __NV_E2M1, cudaRoundNearest)) << (8 * i);
-        }
+        for (int i = 0; i < 4; ++i)
+            q[i] = snap_quotients(make_float2(__uint_as_float(w[4 * h + i] << 16), __uint_as_float(w[4 * h + i] & 0xffff0000u)), r);
+        uint32_t c;
+        asm("{.reg .b8 a, b, c, d;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1; cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5; cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+            "mov.b32 %0, {a, b, c, d};}"
+            : "=r"(c) : "f"(q[0].x), "f"(q[0].y), "f"(q[1].x), "f"(q[1].y), "f"(q[2].x), "f"(q[2].y), "f"(q[3].x), "f"(q[3].y));
         const uint32_t mag = c & 0x77777777u;                     // a zero magnitude keeps no sign
         const uint32_t some = (mag | (mag >> 1) | (mag >> 2)) & 0x11111111u;
         packed[h] = mag | (c & (some << 3));
@@ -113,172 +131,264 @@ __device__ __forceinline__ uint2 fp4_group(const uint32_t (&w)[8], uint32_t &sca
     return make_uint2(packed[0], packed[1]);
 }
 
-__global__ void __launch_bounds__(kApThreads)
+// The rotated ones of channels [c0, c0 + 8) replace w[0 .. 3].
+__device__ __forceinline__ void rope_replace(uint32_t *w, const uint16_t *rot, int c0, int lo, int hi) {
+    if (c0 + 8 <= lo || c0 >= hi) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {                                 // offset and dim are even: pairs of channels
+        const int c = c0 + 2 * i;
+        if (c >= lo && c < hi) w[i] = *reinterpret_cast<const uint32_t *>(rot + c);
+    }
+}
+
+__global__ void __launch_bounds__(kApThreads, kApCtasPerSm)
 append_kv_rope_kernel(const AppendArgs A) {
-    __shared__ uint16_t s_x[kApTok][kDim];                        // rotated channels, at their place
-    __shared__ uint16_t s_k[kApTok][kIdxDim];
+    __shared__ uint16_t s_xs[kApWarps][kApTok][kDim];             // rotated channels, at their place
+    __shared__ uint16_t s_ks[kApWarps][kApTok][kIdxDim];
     pdl_wait();
     pdl_trigger();
-    const int tid = threadIdx.x;
-    const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * kApTok;
-    const bool latent = tid < kApLatent;
-    const int lt = latent ? tid / kApGroups : (tid - kApLatent) >> 2;    // token of the CTA
-    const int g = latent ? tid - lt * kApGroups : tid & 3;               // 16-channel group, or quarter of the key
-    const int64_t tok = tok0 + lt;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t tok0 = (static_cast<int64_t>(blockIdx.x) * kApWarps + warp) * A.tokens;
+    if (tok0 >= A.n) return;
+    const int nt = static_cast<int>(min(static_cast<int64_t>(A.tokens), A.n - tok0));
+    uint16_t (*s_x)[kDim] = s_xs[warp];
+    uint16_t (*s_k)[kIdxDim] = s_ks[warp];
 
-    // this thread's 16 channels (the key's quarter g: channels 8g .. 8g + 7 and 32 + 8g .. 32 + 8g + 7)
-    uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    int64_t slot = -1;
-    const bool mine = tok < A.n && (latent || A.k != nullptr);
-    if (mine) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(latent ? A.x + tok * A.x_stride : A.k + tok * A.k_stride);
-        const uint4 v0 = __ldg(src + (latent ? 2 * g : g)), v1 = __ldg(src + (latent ? 2 * g + 1 : 4 + g));
-        w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w;
-        w[4] = v1.x; w[5] = v1.y; w[6] = v1.z; w[7] = v1.w;
-        slot = A.slots[tok];
-        const int32_t pos = A.pos[tok];
+    // the rows; a key's quarter g is channels 8g .. 8g + 7 and 32 + 8g .. 32 + 8g + 7
+    uint32_t w[kApTok][8], wm[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    auto load = [&](uint32_t (&to)[8], const uint16_t *row, int a, int b) {
+        const uint4 v0 = __ldg(reinterpret_cast<const uint4 *>(row) + a), v1 = __ldg(reinterpret_cast<const uint4 *>(row) + b);
+        to[0] = v0.x; to[1] = v0.y; to[2] = v0.z; to[3] = v0.w;
+        to[4] = v1.x; to[5] = v1.y; to[6] = v1.z; to[7] = v1.w;
+    };
+    const int mt = (lane & 15) >> 2, g = lane & 3;                // token and group, or quarter, of the last step
+#pragma unroll
+    for (int t = 0; t < kApTok; ++t)
+        if (t < nt) load(w[t], A.x + (tok0 + t) * A.x_stride, 2 * lane, 2 * lane + 1);
+    if (mt < nt) {
+        if (lane < 16)
+            load(wm, A.x + (tok0 + mt) * A.x_stride, 64 + 2 * g, 65 + 2 * g);
+        else if (A.k != nullptr)
+            load(wm, A.k + (tok0 + mt) * A.k_stride, g, 4 + g);
+    }
+    int32_t slot = -1, pos = 0;                                   // of token `lane`
+    if (lane < nt) {
+        slot = A.slots[tok0 + lane];
+        pos = A.pos[tok0 + lane];
         if (slot >= 0 && (slot >= A.n_slots || pos < 0 || pos >= kRopeMaxPos)) {
             flag_status(kStatusBounds);
             slot = -1;
         }
     }
 
-    // rotation, one pair per thread and pass
+    // rotation
     const int pairs = A.rope.half + (A.shared_angles ? 0 : A.krope.half);
-    for (int p = tid; p < kApTok * pairs; p += kApThreads) {
-        const int t = p / pairs;
-        int i = p - t * pairs;
-        if (tok0 + t >= A.n) break;                               // later pairs lie in later tokens
-        const int32_t pos = A.pos[tok0 + t];
-        const bool of_x = i < A.rope.half;
-        if (!of_x) i -= A.rope.half;
-        double sn, cs;
-        rope_sincos(pos, __ldg((of_x ? A.rope.inv_freq : A.krope.inv_freq) + i), sn, cs);
-        if (of_x) {
-            const int c = A.rope.first(i), d = A.rope.step();
-            const uint16_t *src = A.x + (tok0 + t) * A.x_stride + c;
-            const uint32_t v = rope_pair(__ldg(src), __ldg(src + d), sn, cs);
-            s_x[t][c] = static_cast<uint16_t>(v);
-            s_x[t][c + d] = static_cast<uint16_t>(v >> 16);
-        }
-        if (!of_x || (A.shared_angles && i < A.krope.half)) {
-            const int c = A.krope.first(i), d = A.krope.step();
-            const uint16_t *src = A.k + (tok0 + t) * A.k_stride + c;
-            const uint32_t v = rope_pair(__ldg(src), __ldg(src + d), sn, cs);
-            s_k[t][c] = static_cast<uint16_t>(v);
-            s_k[t][c + d] = static_cast<uint16_t>(v >> 16);
-        }
-    }
-    __syncthreads();
-
-    // rotated channels replace the loaded ones
-    {
-        const RopeArgs &R = latent ? A.rope : A.krope;
-        const int lo = R.offset, hi = R.offset + 2 * R.half;
-        const uint16_t *rot = latent ? s_x[lt] : s_k[lt];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int c0 = latent ? 16 * g + 8 * h : 32 * h + 8 * g;
-            if (c0 + 8 <= lo || c0 >= hi) continue;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {                         // offset and dim are even: pairs of channels
-                const int c = c0 + 2 * i;
-                if (c >= lo && c < hi) w[4 * h + i] = *reinterpret_cast<const uint32_t *>(rot + c);
+    for (int p = lane; p < pairs; p += 32) {
+        const bool of_x = p < A.rope.half;
+        const int i = of_x ? p : p - A.rope.half;
+        const bool of_k = !of_x || (A.shared_angles && i < A.krope.half);
+        const int xc = A.rope.first(i), xd = A.rope.step(), kc = A.krope.first(i), kd = A.krope.step();
+        const float freq = __ldg((of_x ? A.rope.inv_freq : A.krope.inv_freq) + i);
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t) {
+            const uint16_t *x = A.x + (tok0 + t) * A.x_stride + xc, *k = A.k + (tok0 + t) * A.k_stride + kc;
+            uint16_t xa = 0, xb = 0, ka = 0, kb = 0;
+            if (of_x) xa = __ldg(x), xb = __ldg(x + xd);
+            if (of_k) ka = __ldg(k), kb = __ldg(k + kd);
+            double sn, cs;
+            rope_sincos(A.pos[tok0 + t], freq, sn, cs);
+            if (of_x) {
+                const uint32_t v = rope_pair(xa, xb, sn, cs);
+                s_x[t][xc] = static_cast<uint16_t>(v);
+                s_x[t][xc + xd] = static_cast<uint16_t>(v >> 16);
+            }
+            if (of_k) {
+                const uint32_t v = rope_pair(ka, kb, sn, cs);
+                s_k[t][kc] = static_cast<uint16_t>(v);
+                s_k[t][kc + kd] = static_cast<uint16_t>(v >> 16);
             }
         }
     }
-    if (latent) {
-        if (slot < 0) return;
+    __syncwarp();
+
+    // rotated channels replace the loaded ones; quantise and write
+    const int lo = A.rope.offset, hi = A.rope.offset + 2 * A.rope.half;
+    auto put = [&](uint32_t (&v)[8], int t, int group, int64_t at) {
+        rope_replace(v, s_x[t], 16 * group, lo, hi);
+        rope_replace(v + 4, s_x[t], 16 * group + 8, lo, hi);
         uint32_t sb;
-        const uint2 packed = fp4_group(w, sb);
-        *reinterpret_cast<uint2 *>(A.kv_fp4 + slot * kFp4Bytes + g * 8) = packed;
-        A.kv_scale[slot * kScaleBytes + g] = static_cast<uint8_t>(sb);
-    } else if (A.k != nullptr) {                                  // the whole warp, for the shuffles of a row's lanes
+        const uint2 packed = fp4_group(v, sb);
+        if (at < 0) return;
+        *reinterpret_cast<uint2 *>(A.kv_fp4 + at * kFp4Bytes + group * 8) = packed;
+        A.kv_scale[at * kScaleBytes + group] = static_cast<uint8_t>(sb);
+    };
+#pragma unroll
+    for (int t = 0; t < kApTok; ++t) {
+        const int32_t at = __shfl_sync(0xffffffffu, slot, t);
+        if (t < nt) put(w[t], t, lane, at);
+    }
+    const int32_t at = __shfl_sync(0xffffffffu, slot, mt);
+    if (lane < 16) {
+        put(wm, mt, 32 + g, at);
+    } else if (A.k != nullptr) {
+        rope_replace(wm, s_k[mt], 8 * g, A.krope.offset, A.krope.offset + 2 * A.krope.half);
+        rope_replace(wm + 4, s_k[mt], 32 + 8 * g, A.krope.offset, A.krope.offset + 2 * A.krope.half);
         float sigma;
         uint32_t o[4];
-        fp8_row_codes(w, 0xfu << (threadIdx.x & 28), sigma, o);
-        if (slot < 0) return;
-        const int r = static_cast<int>(slot % kPage);
-        uint8_t *dst = A.kidx + (slot / kPage) * kKidxPageBytes + (r >> 3) * 512 + (r & 7) * 16;
-        // quarter g of the row: 8 bytes of 16-channel block g / 2 and 8 of block 2 + g / 2
-        *reinterpret_cast<uint2 *>(dst + (g >> 1) * 128 + (g & 1) * 8) = make_uint2(o[0], o[1]);
-        *reinterpret_cast<uint2 *>(dst + (2 + (g >> 1)) * 128 + (g & 1) * 8) = make_uint2(o[2], o[3]);
-        if (g == 0) A.kidx_scale[slot] = sigma;
+        fp8_row_codes(wm, 0xffff0000u, sigma, o);
+        if (at >= 0) {
+            const uint32_t page = static_cast<uint32_t>(at) / kPage, r = static_cast<uint32_t>(at) % kPage;
+            uint8_t *dst = A.kidx + static_cast<int64_t>(page) * kKidxPageBytes + (r >> 3) * 512 + (r & 7) * 16;
+            // quarter g of the row: 8 bytes of 16-channel block g / 2 and 8 of block 2 + g / 2
+            *reinterpret_cast<uint2 *>(dst + (g >> 1) * 128 + (g & 1) * 8) = make_uint2(o[0], o[1]);
+            *reinterpret_cast<uint2 *>(dst + (2 + (g >> 1)) * 128 + (g & 1) * 8) = make_uint2(o[2], o[3]);
+            if (g == 0) A.kidx_scale[at] = sigma;
+        }
     }
 }
 
-inline cudaError_t launch_append_kv_rope(const AppendArgs &A, cudaStream_t stream) {
-    return launch_pdl(append_kv_rope_kernel, dim3(static_cast<unsigned>((A.n + kApTok - 1) / kApTok)), dim3(kApThreads),
-                      0, stream, A);
+inline cudaError_t launch_append_kv_rope(AppendArgs A, int sm_count, cudaStream_t stream) {
+    // more tokens per warp once the GPU is full of warps
+    A.tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kApTok, A.n / (kApCtasPerSm * kApWarps * sm_count))));
+    const int64_t per = kApWarps * A.tokens;
+    return launch_pdl(append_kv_rope_kernel, dim3(static_cast<unsigned>((A.n + per - 1) / per)), dim3(kApThreads), 0,
+                      stream, A);
 }
 
 // ------------------------------------------------------------------ K11
 // Query rows [n][heads][dim], in place or to another tensor. A token's angles
-// serve all its heads: a CTA computes them once for the tokens it takes, then
-// rotates pair by pair and, to another tensor, copies the other channels.
+// serve all its heads, so a CTA computes them once for the tokens and heads it
+// takes. Where the rotated range and the distance within a pair are multiples
+// of 8 channels a thread loads 16 bytes (two of them when the row is split in
+// halves) and turns 4 or 8 pairs, and the first load is in flight while the
+// angles are computed; otherwise it goes pair by pair. The other channels are
+// copied, to another tensor only, before the angles. A token's heads are shared
+// out over CTAs while there are fewer CTAs than the GPU holds.
 constexpr int kRrThreads = 256;
+constexpr int kRrTokens = 8;
 constexpr int kRrPairs = 320;                                     // angles held by a CTA (dim / 2 <= 288)
 
 struct RopeRowsArgs {
     const uint16_t *x;
     uint16_t *out;
     int64_t x_stride, out_stride, n;   // elements from token to token
-    int heads, dim, tokens;            // tokens per CTA
+    int heads, dim;
+    int tokens, cta_heads;             // of a CTA
     const int32_t *pos;
     RopeArgs rope;
 };
 
+template <bool kWide>
 __global__ void __launch_bounds__(kRrThreads)
 rope_rows_kernel(const RopeRowsArgs A) {
     __shared__ double2 s_cs[kRrPairs];                            // (cos, sin) of (token, pair)
+    __shared__ bool s_ok[kRrTokens];
     pdl_wait();
     pdl_trigger();
-    const int tid = threadIdx.x, half = A.rope.half;
+    const int tid = threadIdx.x, half = A.rope.half, lo = A.rope.offset, h0 = blockIdx.y * A.cta_heads;
+    const int nh = min(A.cta_heads, A.heads - h0);
     const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * A.tokens;
     const int nt = static_cast<int>(min(static_cast<int64_t>(A.tokens), A.n - tok0));
+    const uint16_t *x = A.x + tok0 * A.x_stride + h0 * A.dim;
+    uint16_t *out = A.out + tok0 * A.out_stride + h0 * A.dim;
+    if (tid < nt) {
+        const int32_t pos = A.pos[tok0 + tid];
+        s_ok[tid] = pos >= 0 && pos < kRopeMaxPos;
+        if (!s_ok[tid]) flag_status(kStatusBounds);
+    }
+    // this thread's first 16 bytes of rotated channels, or first pair
+    const int per_row = !kWide ? half : A.rope.interleaved ? half / 4 : half / 8, items = nt * nh * per_row;
+    uint4 va, vb;
+    int t = 0, i = 0;
+    int64_t from = 0, to = 0;
+    auto load = [&](int p) {
+        const int r = p / per_row, h = r % nh;
+        t = r / nh;
+        i = p - r * per_row;
+        const int c = h * A.dim + (kWide ? lo + 8 * i : A.rope.first(i));
+        from = t * A.x_stride + c;
+        to = t * A.out_stride + c;
+        if (kWide) {
+            va = *reinterpret_cast<const uint4 *>(x + from);
+            if (!A.rope.interleaved) vb = *reinterpret_cast<const uint4 *>(x + from + half);
+        } else {
+            va.x = x[from];
+            vb.x = x[from + A.rope.step()];
+        }
+    };
+    if (tid < items) load(tid);
     for (int p = tid; p < nt * half; p += kRrThreads) {
-        const int t = p / half, i = p - t * half;
-        const int32_t pos = A.pos[tok0 + t];
-        if (i == 0 && (pos < 0 || pos >= kRopeMaxPos)) flag_status(kStatusBounds);
+        const int at = p / half;
         double sn, cs;
-        rope_sincos(pos, __ldg(A.rope.inv_freq + i), sn, cs);
+        rope_sincos(A.pos[tok0 + at], __ldg(A.rope.inv_freq + p - at * half), sn, cs);
         s_cs[p] = make_double2(cs, sn);
     }
     __syncthreads();
-    auto ok = [&](int t) {
-        const int32_t pos = A.pos[tok0 + t];
-        return pos >= 0 && pos < kRopeMaxPos;
-    };
-    // pairs, head by head
-    const int per_tok = A.heads * half;
-    for (int p = tid; p < nt * per_tok; p += kRrThreads) {
-        const int t = p / per_tok, q = p - t * per_tok, h = q / half, i = q - h * half;
-        if (!ok(t)) continue;
-        const int c = h * A.dim + A.rope.first(i), d = A.rope.step();
-        const uint16_t *src = A.x + (tok0 + t) * A.x_stride + c;
-        uint16_t *dst = A.out + (tok0 + t) * A.out_stride + c;
-        const double2 a = s_cs[t * half + i];
-        const uint32_t v = rope_pair(src[0], src[d], a.y, a.x);
-        dst[0] = static_cast<uint16_t>(v);
-        dst[d] = static_cast<uint16_t>(v >> 16);
+    if (A.out != A.x) {
+        if (kWide) {                                              // 8 channels at a time
+            const int rest = (A.dim - 2 * half) / 8;
+            for (int p = tid; p < nt * nh * rest; p += kRrThreads) {
+                const int r = p / rest, ct = r / nh;
+                int c = 8 * (p - r * rest);
+                if (c >= lo) c += 2 * half;
+                c += (r - ct * nh) * A.dim;
+                if (s_ok[ct])
+                    *reinterpret_cast<uint4 *>(out + ct * A.out_stride + c) = *reinterpret_cast<const uint4 *>(x + ct * A.x_stride + c);
+            }
+        } else {
+            const int rest = A.dim / 2 - half;
+            for (int p = tid; p < nt * nh * rest; p += kRrThreads) {
+                const int r = p / rest, ct = r / nh;
+                int c = 2 * (p - r * rest);
+                if (c >= lo) c += 2 * half;
+                c += (r - ct * nh) * A.dim;
+                if (s_ok[ct])
+                    *reinterpret_cast<uint32_t *>(out + ct * A.out_stride + c) = *reinterpret_cast<const uint32_t *>(x + ct * A.x_stride + c);
+            }
+        }
     }
-    if (A.out == A.x) return;
-    // the channels that are not rotated
-    const int lo = A.rope.offset, hi = lo + 2 * half, rest = A.dim - 2 * half;
-    for (int p = tid; p < nt * A.heads * (rest / 2); p += kRrThreads) {
-        const int t = p / (A.heads * (rest / 2)), q = p - t * A.heads * (rest / 2), h = q / (rest / 2);
-        if (!ok(t)) continue;
-        int c = 2 * (q - h * (rest / 2));
-        if (c >= lo) c += hi - lo;
-        *reinterpret_cast<uint32_t *>(A.out + (tok0 + t) * A.out_stride + h * A.dim + c) =
-            *reinterpret_cast<const uint32_t *>(A.x + (tok0 + t) * A.x_stride + h * A.dim + c);
+    for (int p = tid; p < items; p += kRrThreads) {
+        if (p != tid) load(p);
+        if (!s_ok[t]) continue;
+        const double2 *cs = s_cs + t * half;
+        if (!kWide) {
+            const uint32_t v = rope_pair(static_cast<uint16_t>(va.x), static_cast<uint16_t>(vb.x), cs[i].y, cs[i].x);
+            out[to] = static_cast<uint16_t>(v);
+            out[to + A.rope.step()] = static_cast<uint16_t>(v >> 16);
+        } else if (A.rope.interleaved) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t &w = (&va.x)[e];
+                w = rope_pair(static_cast<uint16_t>(w), static_cast<uint16_t>(w >> 16), cs[4 * i + e].y, cs[4 * i + e].x);
+            }
+            *reinterpret_cast<uint4 *>(out + to) = va;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t &a = (&va.x)[e], &b = (&vb.x)[e];
+                const double2 c0 = cs[8 * i + 2 * e], c1 = cs[8 * i + 2 * e + 1];
+                const uint32_t v0 = rope_pair(static_cast<uint16_t>(a), static_cast<uint16_t>(b), c0.y, c0.x);
+                const uint32_t v1 = rope_pair(static_cast<uint16_t>(a >> 16), static_cast<uint16_t>(b >> 16), c1.y, c1.x);
+                a = __byte_perm(v0, v1, 0x5410);
+                b = __byte_perm(v0, v1, 0x7632);
+            }
+            *reinterpret_cast<uint4 *>(out + to) = va;
+            *reinterpret_cast<uint4 *>(out + to + half) = vb;
+        }
     }
 }
 
-inline cudaError_t launch_rope_rows(RopeRowsArgs A, cudaStream_t stream) {
-    A.tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRrPairs / A.rope.half, 8)));
-    return launch_pdl(rope_rows_kernel, dim3(static_cast<unsigned>((A.n + A.tokens - 1) / A.tokens)), dim3(kRrThreads),
-                      0, stream, A);
+inline cudaError_t launch_rope_rows(RopeRowsArgs A, int sm_count, cudaStream_t stream) {
+    // Few CTAs: one token each and its heads shared out, until every SM has two. Many: several tokens each.
+    const int64_t fill = 2 * sm_count;
+    A.tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({A.n / (4 * fill), kRrPairs / A.rope.half, kRrTokens})));
+    const int64_t ctas = (A.n + A.tokens - 1) / A.tokens;
+    const int splits = static_cast<int>(std::min<int64_t>(A.heads, (fill + ctas - 1) / ctas));
+    A.cta_heads = (A.heads + splits - 1) / splits;
+    const dim3 grid(static_cast<unsigned>(ctas), (A.heads + A.cta_heads - 1) / A.cta_heads);
+    const bool wide = A.rope.offset % 8 == 0 && (A.rope.interleaved ? 2 * A.rope.half : A.rope.half) % 8 == 0;
+    return wide ? launch_pdl(rope_rows_kernel<true>, grid, dim3(kRrThreads), 0, stream, A)
+                : launch_pdl(rope_rows_kernel<false>, grid, dim3(kRrThreads), 0, stream, A);
 }
 
 }  // namespace csa2
