@@ -210,6 +210,24 @@ bool rope_ok(const csa2_rope *r, int channels) {
            r->dim <= channels && r->offset <= channels - r->dim && (r->interleaved == 0 || r->interleaved == 1);
 }
 
+// Whether two device ranges share bytes; an absent one shares none.
+bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x != 0 && y != 0 && x < y + b_bytes && y < x + a_bytes;
+}
+
+// The same for two sets of n rows, `row` elements long and a / b strides apart (rows of one wide
+// tensor may lie between the other's).
+bool rows_overlap(const void *a, int64_t a_stride, const void *b, int64_t b_stride, int64_t n, int64_t row, int elem) {
+    const size_t a_bytes = ((n - 1) * a_stride + row) * elem, b_bytes = ((n - 1) * b_stride + row) * elem;
+    if (!overlap(a, a_bytes, b, b_bytes)) return false;
+    if (n == 1 || a_stride != b_stride) return true;
+    const int64_t stride = a_stride * elem;
+    int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)) % stride;
+    if (d < 0) d += stride;
+    return d < row * elem || stride - d < row * elem;
+}
+
 RopeArgs rope_args(const csa2_rope *r) {
     RopeArgs a = {};
     if (r != nullptr) {
@@ -636,6 +654,8 @@ csa2_status csa2_rope_rows(const void *x_bf16, int64_t x_stride, int64_t n_tok, 
     if (!aligned(x_bf16, 16) || !aligned(out_bf16, 16) || x_stride % 8 != 0 || out_stride % 8 != 0 ||
         !aligned(positions, 4) || !aligned(rope->inv_freq, 4))
         return CSA2_ERR_ALIGNMENT;
+    if (x_bf16 != out_bf16 && rows_overlap(x_bf16, x_stride, out_bf16, out_stride, n_tok, row, 2))
+        return CSA2_ERR_INVALID_ARG;
     DeviceInfo *dev = nullptr;
     if (device_info(&dev) != cudaSuccess) return CSA2_ERR_CUDA;
     RopeRowsArgs A = {};
@@ -672,9 +692,20 @@ csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D, const csa2_
         !aligned(lse, 4) || !aligned(page_table, 4) || !aligned(kv_lens, 4) || !aligned(q_offsets, 4) ||
         !aligned(o_own, 16) || !aligned(lse_own, 4))
         return CSA2_ERR_ALIGNMENT;
+    const size_t need = csa2_group_attn_workspace_bytes(N, G), rows = static_cast<size_t>(N) * kHeads;
+    if (!ws || !aligned(ws, 256) || ws_bytes < need) return CSA2_ERR_WORKSPACE;
+    // several CTAs read a token's query and own part while others write its result
+    const struct { const void *p; size_t bytes; } in[] = {{q_bf16, rows * kDim * 2}, {o_own, rows * kDim * 4}, {lse_own, rows * 4}},
+        to[] = {{out_bf16, rows * kDim * 2}, {lse, rows * 4}, {ws, need}};
+    for (int i = 0; i < 3; ++i) {
+        for (const auto &r : in)
+            if (overlap(to[i].p, to[i].bytes, r.p, r.bytes)) return CSA2_ERR_INVALID_ARG;
+        if (overlap(to[i].p, to[i].bytes, to[(i + 1) % 3].p, to[(i + 1) % 3].bytes)) return CSA2_ERR_INVALID_ARG;
+    }
+    const float scale_log2 = softmax_scale * 1.4426950408889634f;
+    if (!std::isfinite(scale_log2)) return CSA2_ERR_INVALID_ARG;
     DeviceInfo *dev = nullptr;
     if (device_info(&dev) != cudaSuccess) return CSA2_ERR_CUDA;
-    if (!ws || !aligned(ws, 256) || ws_bytes < csa2_group_attn_workspace_bytes(N, G)) return CSA2_ERR_WORKSPACE;
     GaArgs A = {};
     A.q = static_cast<const __nv_bfloat16 *>(q_bf16);
     A.kv_fp4 = static_cast<const uint8_t *>(cache->kv_fp4);
@@ -686,7 +717,7 @@ csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D, const csa2_
     A.q_offsets = q_offsets;
     A.N = N;
     A.G = G;
-    A.scale_log2 = softmax_scale * 1.4426950408889634f;
+    A.scale_log2 = scale_log2;
     A.o_own = o_own;
     A.lse_own = lse_own;
     A.out = static_cast<__nv_bfloat16 *>(out_bf16);

@@ -284,7 +284,6 @@ rope_rows_kernel(const RopeRowsArgs A) {
     __shared__ double2 s_cs[kRrPairs];                            // (cos, sin) of (token, pair)
     __shared__ bool s_ok[kRrTokens];
     pdl_wait();
-    pdl_trigger();
     const int tid = threadIdx.x, half = A.rope.half, lo = A.rope.offset, h0 = blockIdx.y * A.cta_heads;
     const int nh = min(A.cta_heads, A.heads - h0);
     const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * A.tokens;
@@ -376,6 +375,7 @@ rope_rows_kernel(const RopeRowsArgs A) {
             *reinterpret_cast<uint4 *>(out + to + half) = vb;
         }
     }
+    __threadfence();
 }
 
 inline cudaError_t launch_rope_rows(RopeRowsArgs A, int sm_count, cudaStream_t stream) {

@@ -455,7 +455,8 @@ csa2_status csa2_append_kv_rope(const void *x_bf16, int64_t x_stride, int64_t n_
  *   x_bf16, out_bf16  device bf16 [n_tok][heads][dim], x_stride / out_stride
  *                     elements from token to token (>= heads * dim, a multiple
  *                     of 8), 16-byte aligned. out_bf16 may be x_bf16 with the
- *                     same stride; otherwise the two must not overlap.
+ *                     same stride; otherwise no row of one may overlap a
+ *                     row of the other (CSA2_ERR_INVALID_ARG).
  *   positions         device int32 [n_tok]; one outside [0, 2^29) sets
  *                     CSA2_ERR_DEVICE_BOUNDS and leaves its token's output as
  *                     it was
@@ -491,7 +492,8 @@ csa2_status csa2_rope_rows(const void *x_bf16, int64_t x_stride, int64_t n_tok, 
  *               Tokens of no group keep what out and lse held.
  *   o_own       device float [N][16][576], or NULL; lse_own float [N][16]
  *   out         device bf16 [N][16][576];  lse device float [N][16]. Neither
- *               may overlap another argument.
+ *               may overlap another argument (CSA2_ERR_INVALID_ARG where it
+ *               meets the query, the own part or the workspace).
  *   ws          device workspace of csa2_group_attn_workspace_bytes(N, G)
  *               bytes, 256-byte aligned, clobbered; calls that can overlap in
  *               time need workspaces of their own
