@@ -16,7 +16,8 @@
 #include "pool.cuh"
 #include "replay.cuh"
 #include "rope.cuh"
-#include "gattn.cuh"
+#include "gattn_few.cuh"
+#include "gattn_merge.cuh"
 
 namespace csa2 {
 
@@ -79,6 +80,9 @@ cudaError_t device_info(DeviceInfo **out) {
         e = cudaFuncSetAttribute(group_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(kGaSmemBytes));
         if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(group_attn_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kGfSmemBytes));
+        if (e != cudaSuccess) return e;
         // One shared-memory carveout for every kernel of the path, so that
         // consecutive launches do not reconfigure the SMs' L1 / shared split.
         const void *kernels[] = {reinterpret_cast<const void *>(quant_kv_fp4_kernel),
@@ -96,6 +100,7 @@ cudaError_t device_info(DeviceInfo **out) {
                                  reinterpret_cast<const void *>(rope_rows_kernel<true>),
                                  reinterpret_cast<const void *>(rope_rows_kernel<false>),
                                  reinterpret_cast<const void *>(group_attn_kernel),
+                                 reinterpret_cast<const void *>(group_attn_few_kernel),
                                  reinterpret_cast<const void *>(group_attn_merge_kernel)};
         for (const void *kf : kernels) {
             e = cudaFuncSetAttribute(kf, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -722,14 +727,17 @@ csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D, const csa2_
     A.lse_own = lse_own;
     A.out = static_cast<__nv_bfloat16 *>(out_bf16);
     A.lse = lse;
-    A.tok_slots = std::min(N, kGaTok);
+    // Both forms take any groups; with few tokens in each the wide one's rows go unused.
+    A.few = N <= kGfTok * G;
+    A.tok_slots = std::min(N, A.few ? kGfTok : kGaTok);
     uint8_t *base = static_cast<uint8_t *>(ws);
     A.plan = reinterpret_cast<GaPlan *>(base);
     A.part_ml = reinterpret_cast<float2 *>(base + ga_plan_bytes());
     A.part_o = reinterpret_cast<float *>(base + ga_plan_bytes() + ga_ml_bytes(A.tok_slots));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int ctas = std::min(dev->sm_count, kGaMaxCtas);
-    cudaError_t e = launch_pdl(group_attn_kernel, dim3(ctas), dim3(kGaThreads), kGaSmemBytes, st, A);
+    const cudaError_t e = A.few ? launch_pdl(group_attn_few_kernel, dim3(ctas), dim3(kGaThreads), kGfSmemBytes, st, A)
+                                : launch_pdl(group_attn_kernel, dim3(ctas), dim3(kGaThreads), kGaSmemBytes, st, A);
     if (e != cudaSuccess) return CSA2_ERR_CUDA;
     return cuda_status(launch_pdl(group_attn_merge_kernel, dim3(kGmCtasPerSm * ctas), dim3(kGmThreads), 0, st, A));
 }

@@ -67,9 +67,16 @@ constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a 
 // A block's nine chunks are filled, multiplied and released in three rounds, in
 // the order in which O's MMAs are done with them: 2 r, 2 r + 1 and 6 + r.
 constexpr int kGaRounds = 3;
-constexpr int kGaGap = 5;                                          // steps a row tile counts for beside its blocks
+constexpr int kGaGap = 5;
 constexpr float kGaSlack = 8.0f;                                   // log2 units a block may exceed the reference
 static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 96, "tensor memory is full; pieces of 64, 32, 64 and 32 channels");
+
+// A row tile of kT tokens, blocks of kB keys, and what a row tile costs beside
+// its blocks (query in, result out), in blocks, so that ranges with many short
+// tiles are not the longest.
+template <int kT, int kB, int kG>
+struct GaForm { static constexpr int kTok = kT, kBlk = kB, kGap = kG; };
+using GaWide = GaForm<kGaTok, kGaBlk, kGaGap>;
 
 struct GaArgs {
     const __nv_bfloat16 *q;            // [N][16][576]
@@ -85,9 +92,11 @@ struct GaArgs {
     __nv_bfloat16 *out;                // [N][16][576]
     float *lse;                        // [N][16]
     struct GaPlan *plan;
-    float *part_o;                     // [2 * ranges][tok_slots][144][16][4]: 4 channels of 16 heads together
+    // [2 * ranges][tok_slots][144][16][4], 4 channels of 16 heads together; with few tokens [..][16][576]
+    float *part_o;
     float2 *part_ml;                   // [2 * ranges][tok_slots * 16]: (m in the log2 domain, l)
-    int tok_slots;                     // min(8, N)
+    int tok_slots;                     // min(8, N), with few tokens min(4, N)
+    int few;                           // the form for few tokens per group
 };
 
 // What K13 has to know of K12's ranges.
@@ -106,6 +115,7 @@ struct GaGroup { int tok0, n, T, blocks; };
 // Group g as the kernel takes it: bounds outside [0, N] leave it without
 // tokens, a bad length without entries. A group without entries still has one
 // (empty) block per row tile, which writes its tokens' own parts.
+template <class F>
 __device__ __forceinline__ GaGroup ga_group(const GaArgs &A, int g, bool report) {
     GaGroup r;
     r.tok0 = __ldg(A.q_offsets + g);
@@ -122,15 +132,14 @@ __device__ __forceinline__ GaGroup ga_group(const GaArgs &A, int g, bool report)
         r.T = 0;
     }
     if (bad && report) flag_status(kStatusBounds);
-    r.blocks = max(1, (r.T + kPage - 1) / kPage);
+    r.blocks = max(1, (r.T + F::kBlk - 1) / F::kBlk);
     return r;
 }
 
-// A row tile's steps: its blocks, after kGaGap steps that stand for what it
-// costs besides (query in, result out), so that ranges with many short tiles
-// are not the longest.
+// A group's steps: for each row tile its blocks, after the gap.
+template <class F>
 __device__ __forceinline__ int64_t ga_steps(const GaGroup &g) {
-    return static_cast<int64_t>((g.n + kGaTok - 1) / kGaTok) * (kGaGap + g.blocks);
+    return static_cast<int64_t>((g.n + F::kTok - 1) / F::kTok) * (F::kGap + g.blocks);
 }
 
 // One row tile's blocks [k0, k1) of a CTA's range.
@@ -139,25 +148,26 @@ struct GaSeg {
 };
 
 // Walks a range segment by segment; every role of the CTA does so by itself.
+template <class F>
 struct GaWalk {
     int64_t left;                      // steps to go
     int g, tile, k;                    // group, row tile of the group, step of the row tile
     __device__ __forceinline__ bool next(const GaArgs &A, GaSeg &s) {
         while (left > 0) {
-            GaGroup grp = ga_group(A, g, false);
-            while (tile * kGaTok >= grp.n) {
+            GaGroup grp = ga_group<F>(A, g, false);
+            while (tile * F::kTok >= grp.n) {
                 if (++g >= A.G) return false;
-                grp = ga_group(A, g, false);
+                grp = ga_group<F>(A, g, false);
                 tile = 0;
             }
-            const int len = kGaGap + grp.blocks, end = left < len - k ? k + static_cast<int>(left) : len;
+            const int len = F::kGap + grp.blocks, end = left < len - k ? k + static_cast<int>(left) : len;
             s.g = g;
-            s.tok0 = grp.tok0 + tile * kGaTok;
-            s.ntok = min(kGaTok, grp.n - tile * kGaTok);
+            s.tok0 = grp.tok0 + tile * F::kTok;
+            s.ntok = min(F::kTok, grp.n - tile * F::kTok);
             s.T = grp.T;
             s.blocks = grp.blocks;
-            s.k0 = max(0, k - kGaGap);
-            s.k1 = max(0, end - kGaGap);
+            s.k0 = max(0, k - F::kGap);
+            s.k1 = max(0, end - F::kGap);
             left -= end - k;
             k = 0;
             ++tile;
@@ -183,7 +193,7 @@ struct GaSmem {
     float l[kGaRows];
     int64_t scan[kGaThreads / 32], start, total;
     int start_g;
-    GaWalk walk;
+    GaWalk<GaWide> walk;
 };
 constexpr size_t kGaSmemBytes = sizeof(GaSmem);
 static_assert(kGaSmemBytes <= 232448, "one CTA per SM");
@@ -302,12 +312,13 @@ __device__ __forceinline__ float2 ga_add2(float2 a, float2 b) {
 // The first step of this CTA's range (its group, and that group's first step)
 // and the total: a block scan over the groups, again over the chunks of 512
 // when there are more.
-__device__ __forceinline__ void ga_locate(const GaArgs &A, GaSmem &sm) {
+template <class F, class Smem>
+__device__ __forceinline__ void ga_locate(const GaArgs &A, Smem &sm) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kWarps = kGaThreads / 32;
     int64_t base = 0, begin = 0, mine = 0;
     auto scan = [&](int g0, bool report) {                // begin, mine of group g0 + tid; base moves past the chunk
-        mine = g0 + tid < A.G ? ga_steps(ga_group(A, g0 + tid, report)) : 0;
+        mine = g0 + tid < A.G ? ga_steps<F>(ga_group<F>(A, g0 + tid, report)) : 0;
         int64_t incl = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -340,20 +351,55 @@ __device__ __forceinline__ void ga_locate(const GaArgs &A, GaSmem &sm) {
     }
 }
 
-// Query tile -> f16 under a power-of-two exponent per row, one token per warp:
-// a warp's loads are 64-byte runs of 8 rows and its stores whole 128-byte core
+// Finds the CTA's range (sm.walk, complete after the next barrier) and leaves
+// what K13 has to know of it; false without one.
+template <class F, class Smem>
+__device__ __forceinline__ bool ga_begin(const GaArgs &A, Smem &sm) {
+    const int tid = threadIdx.x, range = blockIdx.x;
+    ga_locate<F>(A, sm);
+    __syncthreads();
+    const int64_t total = sm.total;
+    const int ranges = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    if (range == 0 && tid == 0) {
+        A.plan->total = total;
+        A.plan->ranges = ranges;
+    }
+    if (range >= ranges) return false;
+    if (tid == 0) {
+        const int64_t at = ga_range(total, range, ranges), local = at - sm.start;
+        const GaGroup grp = ga_group<F>(A, sm.start_g, false);
+        const int len = F::kGap + grp.blocks;
+        GaWalk<F> w;
+        w.left = ga_range(total, range + 1, ranges) - at;
+        w.g = sm.start_g;
+        w.tile = static_cast<int>(local / len);
+        w.k = static_cast<int>(local - static_cast<int64_t>(w.tile) * len);
+        sm.walk = w;
+        GaPlan::Tile &t = A.plan->first[range];
+        t.begin = at - w.k + F::kGap;
+        t.blocks = grp.blocks;
+        t.tok0 = grp.tok0 + w.tile * F::kTok;
+        t.ntok = min(F::kTok, grp.n - w.tile * F::kTok);
+    }
+    return true;
+}
+
+// kHalves x 8 heads of a token of the query tile, from head0 on, -> f16 under a
+// power-of-two exponent per row: a warp's loads are 64-byte runs of 8 rows and its stores whole 128-byte core
 // matrices. The exponent is 0 as a rule, so the rows are stored as they come
 // and again only where the largest magnitude asks for another one. Kept small:
 // the code runs once per row tile, at the pace of the instruction fetch.
-__device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaSeg &s, int warp, int lane) {
-    const bool some = warp < s.ntok;
+template <int kSlab, int kHalves>
+__device__ __forceinline__ void ga_load_q(const GaArgs &A, uint8_t *tile, float *scale, const GaSeg &s, int tok, int head0,
+                                          int lane) {
+    const bool some = tok < s.ntok;
     // a negative softmax scale turns the query round, so that the largest score has the largest logit
     const float sign = copysignf(1.0f, A.scale_log2);
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-        const int h = half * 8 + (lane & 7), row = warp * kHeads + h, part = lane >> 3;
-        const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (static_cast<int64_t>(s.tok0 + (some ? warp : 0)) * kHeads + h) * kDim) + part;
-        uint8_t *dst = sm.q + part * kGaQSlab + row * 16;
+    for (int half = 0; half < kHalves; ++half) {
+        const int h = head0 + half * 8 + (lane & 7), row = tok * kHeads + h, part = lane >> 3;
+        const uint4 *src = reinterpret_cast<const uint4 *>(A.q + (static_cast<int64_t>(s.tok0 + (some ? tok : 0)) * kHeads + h) * kDim) + part;
+        uint8_t *dst = tile + part * kSlab + row * 16;
         float mx, down = sign;
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {
@@ -373,7 +419,7 @@ __device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaS
                         const float2 f = bf16x2_f32(w);
                         o[e] = f32x2_f16x2(f.x * down, f.y * down);
                     }
-                    *reinterpret_cast<uint4 *>(dst + 4 * (u0 + u) * kGaQSlab) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(dst + 4 * (u0 + u) * kSlab) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
             mx = __uint_as_float(max(m2 & 0xffff0000u, m2 << 16));
@@ -381,7 +427,7 @@ __device__ __forceinline__ void ga_load_q(const GaArgs &A, GaSmem &sm, const GaS
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const int eq = mx < INFINITY ? f16_exponent(mx) : 0;   // a row with inf or NaN stays one
             // never 0: entries that do not count have a score of -inf, which has to stay one
-            if (part == 0) sm.scale[row] = fmaxf(fabsf(A.scale_log2) * exp2f(static_cast<float>(eq)), 1e-30f);
+            if (part == 0) scale[row] = fmaxf(fabsf(A.scale_log2) * exp2f(static_cast<float>(eq)), 1e-30f);
             if (!__any_sync(0xffffffffu, eq != 0)) break;
             down = sign * exp2f(static_cast<float>(-eq));
         }
@@ -437,7 +483,7 @@ __device__ __forceinline__ void ga_write16(const GaArgs &A, int64_t row, int ch,
     dst[1] = make_uint4(b[4], b[5], b[6], b[7]);
 }
 
-__device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk walk, int warp, int lane) {
+__device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk<GaWide> walk, int warp, int lane) {
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;      // keys 32 half ..; tile row
     const uint32_t tm = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int pair_bar = 1 + (warp & 3);                           // the two warps of the same rows
@@ -452,7 +498,7 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
         }
         const int32_t *pages = A.page_table + static_cast<int64_t>(s.g) * A.max_pages;
         int page = __ldg(pages + s.k0);
-        ga_load_q(A, sm, s, warp, lane);
+        ga_load_q<kGaQSlab, 2>(A, sm.q, sm.scale, s, warp, 0, lane);
         fence_proxy_async_smem();
         asm volatile("bar.sync 5, 256;" ::: "memory");             // scales of all rows; the tile is whole
         if (threadIdx.x == 0) mbar_arrive(&sm.q_full);
@@ -605,7 +651,7 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk w
 
 // Walks the blocks of a range's segments with entries, one ahead with the page.
 struct GaBlocks {
-    GaWalk walk;
+    GaWalk<GaWide> walk;
     GaSeg s;
     int kb, page;                      // the block at hand; its page
     __device__ __forceinline__ bool segment(const GaArgs &A) {
@@ -642,7 +688,7 @@ struct GaRaw {
     uint32_t s[2];                     // their two scales each
 };
 
-__device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk walk, int warp, int lane) {
+__device__ __forceinline__ void ga_dequant(const GaArgs &A, GaSmem &sm, GaWalk<GaWide> walk, int warp, int lane) {
     const int place = warp % 3, key = 32 * (warp / 3) + (lane & 15), part = lane >> 4;   // the lane's first key, and 16 on
     uint8_t *const dst0 = sm.k + 4 * part * kGaKSlab + key * 16;
     auto chunk_of = [&](int round) { return place < 2 ? 2 * round + place : 6 + round; };
@@ -719,7 +765,7 @@ __device__ __forceinline__ void ga_pv(uint32_t one, uint32_t d, uint32_t v_lo, u
     ga_mma_ts<id, kGaPCol + 24, 48, hi>(one, d, v_lo, 1u);
 }
 
-__device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk walk) {
+__device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk<GaWide> walk) {
     const uint32_t one = ga_elect() ? 1u : 0u;
     const uint32_t d_q = ga_desc_lo(sm.q, kGaQSlab), d_k = ga_desc_lo(sm.k, kGaKSlab), d_v = ga_desc_lo(sm.k, 128);
     GaWait wait;
@@ -778,7 +824,7 @@ __global__ void __launch_bounds__(kGaThreads, 1)
 group_attn_kernel(const GaArgs A) {
     extern __shared__ __align__(1024) uint8_t ga_raw[];
     GaSmem &sm = *reinterpret_cast<GaSmem *>(ga_raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, range = blockIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.s_full, 1);
@@ -795,31 +841,7 @@ group_attn_kernel(const GaArgs A) {
         fence_mbar_init();
     }
     pdl_wait();
-    ga_locate(A, sm);
-    __syncthreads();
-    const int64_t total = sm.total;
-    const int ranges = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-    if (range == 0 && tid == 0) {
-        A.plan->total = total;
-        A.plan->ranges = ranges;
-    }
-    if (range >= ranges) return;
-    if (tid == 0) {
-        const int64_t at = ga_range(total, range, ranges), local = at - sm.start;
-        const GaGroup grp = ga_group(A, sm.start_g, false);
-        const int len = kGaGap + grp.blocks;
-        GaWalk w;
-        w.left = ga_range(total, range + 1, ranges) - at;
-        w.g = sm.start_g;
-        w.tile = static_cast<int>(local / len);
-        w.k = static_cast<int>(local - static_cast<int64_t>(w.tile) * len);
-        sm.walk = w;
-        GaPlan::Tile &t = A.plan->first[range];
-        t.begin = at - w.k + kGaGap;
-        t.blocks = grp.blocks;
-        t.tok0 = grp.tok0 + w.tile * kGaTok;
-        t.ntok = min(kGaTok, grp.n - w.tile * kGaTok);
-    }
+    if (!ga_begin<GaWide>(A, sm)) return;
     if (warp == kGaMmaWarp) {
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();
@@ -827,7 +849,7 @@ group_attn_kernel(const GaArgs A) {
     }
     __syncthreads();
     tc_fence_after();
-    const GaWalk walk = sm.walk;
+    const GaWalk<GaWide> walk = sm.walk;
     if (warp < kGaSoftWarps) {
         ga_regs_up<kGaSoftRegs>();
         ga_softmax(A, sm, walk, warp, lane);
@@ -846,185 +868,6 @@ group_attn_kernel(const GaArgs A) {
         tc_fence_after();
         tmem_dealloc(sm.tmem, 512);
     }
-}
-
-// ------------------------------------------------------------------ K13
-// Joins the partials of the row tiles that K12's ranges cut, with the own
-// part. Memory-bound in principle (36,864 B per partial and token, L2), latency
-// bound per unit of work, so a unit is one slice of a token's channels: all
-// 192, 64 or 16 of them, the smaller the fewer tokens there are to fill the
-// GPU, and the first partials are loaded together with the maxima and sums. A
-// thread takes 4 channels of a head; with 16 channels the four groups of 64
-// threads take every fourth partial each.
-constexpr int kGmThreads = 256;
-constexpr int kGmCtasPerSm = 4;
-constexpr int kGmBatch = 8;                                        // partials loaded together
-
-struct GmSmem {
-    GaPlan::Tile first[kGaMaxCtas];
-    alignas(16) float2 ml[kGaMaxCtas + 1][kHeads];                 // (m, l) of a partial, then (its weight, -)
-    float red[2][kGmThreads / kHeads][kHeads];
-    float4 sum[4][64];
-    int before[kGaMaxCtas + 1];                                    // tokens up to a boundary
-    int warp_sum[kGmThreads / 32];
-};
-
-// kPer x 64 channels of a token from col0 on, or (kPer = 0) 16 channels.
-template <int kPer>
-__device__ __forceinline__ void gm_slice(const GaArgs &A, GmSmem &sm, int c0, int n, int slot0, int tok, int64_t row,
-                                         int col0, bool write_lse) {
-    constexpr int kGroups = kPer == 0 ? 4 : 1, kV = kPer == 0 ? 1 : kPer, kAtOnce = kPer == 3 ? 2 : kGmBatch;
-    const int tid = threadIdx.x, h = tid & (kHeads - 1), at = tid >> 4;
-    const int grp = kPer == 0 ? tid >> 6 : 0, c4 = col0 / 4 + (kPer == 0 ? (tid & 63) >> 4 : at);
-    const float4 *po = reinterpret_cast<const float4 *>(A.part_o) + static_cast<int64_t>(tok) * (kDim * kHeads / 4) + c4 * kHeads + h;
-    auto slot = [&](int p) { return static_cast<int64_t>(p == 0 ? slot0 : 2 * (c0 + p)) * A.tok_slots; };
-    float4 v[kAtOnce][kV];
-    auto load = [&](int b) {                                       // partials b, b + kGroups, ..
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const int p = min(b + i * kGroups, n - 1);             // past the end: the last one again, weight 0
-#pragma unroll
-            for (int k = 0; k < kV; ++k) v[i][k] = __ldcg(po + slot(p) * (kDim * kHeads / 4) + k * (16 * kHeads));
-        }
-    };
-    constexpr int kLanes = kGmThreads / kHeads;
-    for (int p = at; p < n; p += kLanes)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;"
-                     ::"r"(smem_u32(&sm.ml[p][h])), "l"(&A.part_ml[(slot(p) + tok) * kHeads + h]) : "memory");
-    cp_async_commit();
-    load(grp);
-    // ---- weights
-    const float own = A.lse_own ? __ldg(A.lse_own + row + h) * 1.4426950408889634f : -INFINITY;
-    float mx = own;
-    cp_async_wait<0>();
-    for (int p = at; p < n; p += kLanes) mx = fmaxf(mx, sm.ml[p][h].x);
-    sm.red[0][at][h] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kLanes; ++i) mx = fmaxf(mx, sm.red[0][i][h]);
-    const float ref = mx == -INFINITY ? 0.0f : mx;
-    float l = 0.0f;
-    for (int p = at; p < n; p += kLanes) {
-        const float w = ga_ex2(sm.ml[p][h].x - ref);
-        l += sm.ml[p][h].y * w;
-        sm.ml[p][h].x = w;
-    }
-    sm.red[1][at][h] = l;
-    __syncthreads();
-    const float wo = ga_ex2(own - ref);
-    l = wo;
-#pragma unroll
-    for (int i = 0; i < kLanes; ++i) l += sm.red[1][i][h];
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;                 // a NaN stays one
-    const float fo = wo > 0.0f ? wo * inv : 0.0f;                  // nothing to read without an own part
-    if (write_lse && at == 0) A.lse[row + h] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
-    // ---- the channels
-    float4 a[kV];
-#pragma unroll
-    for (int k = 0; k < kV; ++k) a[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int b = grp; b < n; b += kAtOnce * kGroups) {
-        if (b != grp) load(b);
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const int p = b + i * kGroups;
-            const float w = p < n ? sm.ml[p][h].x : 0.0f;
-#pragma unroll
-            for (int k = 0; k < kV; ++k) {
-                a[k].x += w * v[i][k].x;
-                a[k].y += w * v[i][k].y;
-                a[k].z += w * v[i][k].z;
-                a[k].w += w * v[i][k].w;
-            }
-        }
-    }
-    if constexpr (kPer == 0) {
-        sm.sum[grp][tid & 63] = a[0];
-        __syncthreads();
-        if (grp == 0)
-#pragma unroll
-            for (int i = 1; i < 4; ++i) {
-                const float4 o = sm.sum[i][tid];
-                a[0].x += o.x;
-                a[0].y += o.y;
-                a[0].z += o.z;
-                a[0].w += o.w;
-            }
-    }
-    if (grp == 0)
-#pragma unroll
-        for (int k = 0; k < kV; ++k) {
-            const int64_t to = (row + h) * kDim + (c4 + 16 * k) * 4;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (fo != 0.0f) o = __ldg(reinterpret_cast<const float4 *>(A.o_own + to));
-            const __nv_bfloat162 x = __floats2bfloat162_rn(a[k].x * inv + fo * o.x, a[k].y * inv + fo * o.y);
-            const __nv_bfloat162 y = __floats2bfloat162_rn(a[k].z * inv + fo * o.z, a[k].w * inv + fo * o.w);
-            *reinterpret_cast<uint2 *>(A.out + to) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-        }
-    __syncthreads();
-}
-
-__global__ void __launch_bounds__(kGmThreads, kGmCtasPerSm)
-group_attn_merge_kernel(const GaArgs A) {
-    __shared__ GmSmem sm;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_wait();
-    pdl_trigger();
-    const int64_t total = __ldcg(&A.plan->total);
-    const int ranges = __ldcg(&A.plan->ranges);
-    GaPlan::Tile mine = {};
-    if (tid < kGaMaxCtas) {                                        // beyond the ranges: whatever is there, not looked at
-        mine.begin = __ldcg(&A.plan->first[tid].begin);
-        mine.blocks = __ldcg(&A.plan->first[tid].blocks);
-        mine.tok0 = __ldcg(&A.plan->first[tid].tok0);
-        mine.ntok = __ldcg(&A.plan->first[tid].ntok);
-        sm.first[tid] = mine;
-    }
-    // The range boundary c cuts the row tile of range c's first step when the
-    // tile begins before it; the first such boundary of a tile stands for it.
-    int incl = 0;
-    if (tid > 0 && tid < ranges && mine.begin < ga_range(total, tid, ranges) && mine.begin >= ga_range(total, tid - 1, ranges))
-        incl = mine.ntok;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-    }
-    if (lane == 31) sm.warp_sum[warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += sm.warp_sum[w];
-    if (tid < kGaMaxCtas) sm.before[tid + 1] = incl;
-    if (tid == 0) sm.before[0] = 0;
-    __syncthreads();
-    const int tokens = sm.before[kGaMaxCtas];
-    // slices of 16 channels while 36 of them per token fit one wave of CTAs, then of 64, then of 192
-    const int grid = static_cast<int>(gridDim.x);
-    const int per = tokens * 36 <= grid ? 36 : tokens * 9 <= 2 * grid ? 9 : 3;
-    for (int unit = blockIdx.x; unit < tokens * per; unit += grid) {
-        const int ut = unit / per, slice = unit - ut * per;
-        int lo = 0, hi = kGaMaxCtas;                               // the boundary: before[c] <= ut < before[c + 1]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (sm.before[mid] <= ut) lo = mid; else hi = mid;
-        }
-        const GaPlan::Tile &t = sm.first[lo];
-        const int tok = ut - sm.before[lo];
-        // ranges c0 = lo - 1 (which begins the tile) to the last c with total * c / ranges < the tile's end; a range's
-        // first tile is in its slot 0
-        const int c0 = lo - 1, n = static_cast<int>(((t.begin + t.blocks) * ranges - 1) / total) - c0 + 1;
-        const int slot0 = 2 * c0 + (ga_range(total, c0, ranges) < t.begin - kGaGap ? 1 : 0);
-        const int64_t row = static_cast<int64_t>(t.tok0 + tok) * kHeads;
-        if (per == 36) gm_slice<0>(A, sm, c0, n, slot0, tok, row, slice * 16, slice == 0);
-        else if (per == 9) gm_slice<1>(A, sm, c0, n, slot0, tok, row, slice * 64, slice == 0);
-        else gm_slice<3>(A, sm, c0, n, slot0, tok, row, slice * 192, slice == 0);
-    }
-}
-
-// Workspace: the plan, then two partials per range.
-inline size_t ga_plan_bytes() { return (sizeof(GaPlan) + 255) / 256 * 256; }
-inline size_t ga_ml_bytes(int tok_slots) { return static_cast<size_t>(2 * kGaMaxCtas) * tok_slots * kHeads * sizeof(float2); }
-inline size_t ga_ws_bytes(int tok_slots) {
-    return ga_plan_bytes() + ga_ml_bytes(tok_slots) + static_cast<size_t>(2 * kGaMaxCtas) * tok_slots * kHeads * kDim * 4;
 }
 
 }  // namespace csa2
