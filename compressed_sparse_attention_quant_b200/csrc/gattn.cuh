@@ -351,37 +351,25 @@ __device__ __forceinline__ void ga_locate(const GaArgs &A, Smem &sm) {
     }
 }
 
-// Finds the CTA's range (sm.walk, complete after the next barrier) and leaves
-// what K13 has to know of it; false without one.
+// One thread: the walk of the CTA's range, complete after the next barrier,
+// and what K13 has to know of its first row tile.
 template <class F, class Smem>
-__device__ __forceinline__ bool ga_begin(const GaArgs &A, Smem &sm) {
-    const int tid = threadIdx.x, range = blockIdx.x;
-    ga_locate<F>(A, sm);
-    __syncthreads();
-    const int64_t total = sm.total;
-    const int ranges = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-    if (range == 0 && tid == 0) {
-        A.plan->total = total;
-        A.plan->ranges = ranges;
-    }
-    if (range >= ranges) return false;
-    if (tid == 0) {
-        const int64_t at = ga_range(total, range, ranges), local = at - sm.start;
-        const GaGroup grp = ga_group<F>(A, sm.start_g, false);
-        const int len = F::kGap + grp.blocks;
-        GaWalk<F> w;
-        w.left = ga_range(total, range + 1, ranges) - at;
-        w.g = sm.start_g;
-        w.tile = static_cast<int>(local / len);
-        w.k = static_cast<int>(local - static_cast<int64_t>(w.tile) * len);
-        sm.walk = w;
-        GaPlan::Tile &t = A.plan->first[range];
-        t.begin = at - w.k + F::kGap;
-        t.blocks = grp.blocks;
-        t.tok0 = grp.tok0 + w.tile * F::kTok;
-        t.ntok = min(F::kTok, grp.n - w.tile * F::kTok);
-    }
-    return true;
+__device__ __forceinline__ void ga_begin(const GaArgs &A, Smem &sm, int64_t total, int ranges) {
+    const int range = blockIdx.x;
+    const int64_t at = ga_range(total, range, ranges), local = at - sm.start;
+    const GaGroup grp = ga_group<F>(A, sm.start_g, false);
+    const int len = F::kGap + grp.blocks;
+    GaWalk<F> w;
+    w.left = ga_range(total, range + 1, ranges) - at;
+    w.g = sm.start_g;
+    w.tile = static_cast<int>(local / len);
+    w.k = static_cast<int>(local - static_cast<int64_t>(w.tile) * len);
+    sm.walk = w;
+    GaPlan::Tile &t = A.plan->first[range];
+    t.begin = at - w.k + F::kGap;
+    t.blocks = grp.blocks;
+    t.tok0 = grp.tok0 + w.tile * F::kTok;
+    t.ntok = min(F::kTok, grp.n - w.tile * F::kTok);
 }
 
 // kHalves x 8 heads of a token of the query tile, from head0 on, -> f16 under a
@@ -841,7 +829,16 @@ group_attn_kernel(const GaArgs A) {
         fence_mbar_init();
     }
     pdl_wait();
-    if (!ga_begin<GaWide>(A, sm)) return;
+    ga_locate<GaWide>(A, sm);
+    __syncthreads();
+    const int64_t total = sm.total;
+    const int ranges = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    if (blockIdx.x == 0 && tid == 0) {
+        A.plan->total = total;
+        A.plan->ranges = ranges;
+    }
+    if (static_cast<int>(blockIdx.x) >= ranges) return;
+    if (tid == 0) ga_begin<GaWide>(A, sm, total, ranges);
     if (warp == kGaMmaWarp) {
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();

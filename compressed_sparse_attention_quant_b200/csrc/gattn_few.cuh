@@ -14,7 +14,7 @@
 // and MN-major for O; P is written by the softmax threads as slabs of 8 rows
 // (16 bytes) per key, MN-major.
 //   warps 0-7   load the query tile, then per block the softmax: thread = key,
-//               warps 0-3 the first two tokens and 4-7 the others. A thread
+//               warps 0-3 the first half of the rows and 4-7 the other. A thread
 //               does not see a row's other keys, and does not have to: it
 //               compares its scores with the rows' references, and only when
 //               one of them exceeds its reference by more than 8 do all take
@@ -30,7 +30,7 @@
 namespace csa2 {
 
 constexpr int kGfTok = 4, kGfRows = kGfTok * kHeads;               // 64
-constexpr int kGfBlk = 112, kGfGap = 3;
+constexpr int kGfBlk = 112, kGfGap = 2;
 using GaFew = GaForm<kGfTok, kGfBlk, kGfGap>;
 constexpr int kGfDeqWarps = 7;
 constexpr int kGfQSlab = kGfRows * 16, kGfKSlab = kGfBlk * 16;     // 1,024 and 1,792 B
@@ -60,19 +60,56 @@ struct GfSmem {
 constexpr size_t kGfSmemBytes = sizeof(GfSmem);
 static_assert(kGfSmemBytes <= 232448 && kGfRows * kGfBlk * 2 >= 256, "one CTA per SM");
 
-// Lane c gets the maximum (or sum) over the lanes of x[c].
+// 32 lanes x 8 columns.
+__device__ __forceinline__ void gf_tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void gf_tmem_st8(uint32_t taddr, const float (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
+                 "tcgen05.wait::st.sync.aligned;"
+                 ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
+// K12's MMA from shared memory with the number of columns at run time: what
+// the rows of absent tokens would read is left to the dequantising warps.
+template <uint32_t kA, uint32_t kAHi, uint32_t kB, uint32_t kBHi>
+__device__ __forceinline__ void gf_mma_ss(uint32_t one, uint32_t idesc, uint32_t d, uint32_t a_lo, uint32_t b_lo,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.u32 e, %9, 0;\n\tsetp.ne.u32 p, %2, 0;\n\tadd.u32 a, %0, %5;\n\tadd.u32 b, %1, %7;\n\t"
+        "mov.b64 da, {a, %6};\n\tmov.b64 db, {b, %8};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%3], da, db, %4, p;\n\t}"
+        ::"r"(a_lo), "r"(b_lo), "r"(accumulate), "r"(d), "r"(idesc), "n"(kA), "n"(kAHi), "n"(kB), "n"(kBHi), "r"(one)
+        : "memory");
+}
+
+// Lane c < 8 n (n = 1 .. 4) gets the maximum (or sum) over the lanes of x[c]:
+// each step halves the columns and doubles the lanes that a value stands for;
+// with few columns the first steps come last, on one value.
 template <bool kMax>
-__device__ __forceinline__ float gf_across(float (&x)[32], int lane) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) {
+__device__ __forceinline__ float gf_across(float (&x)[32], int n, int lane) {
+    auto join = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
+    auto halve = [&](auto d_) {
+        constexpr int d = decltype(d_)::value;
         const bool up = lane & d;
 #pragma unroll
-        for (int i = 0; i < d; ++i) {
-            const float keep = up ? x[i + d] : x[i], other = __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + d], d);
-            x[i] = kMax ? fmaxf(keep, other) : keep + other;
-        }
-    }
-    return x[0];
+        for (int i = 0; i < d; ++i)
+            x[i] = join(up ? x[i + d] : x[i], __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + d], d));
+    };
+    if (n > 2) halve(std::integral_constant<int, 16>{});
+    if (n > 1) halve(std::integral_constant<int, 8>{});
+    halve(std::integral_constant<int, 4>{});
+    halve(std::integral_constant<int, 2>{});
+    halve(std::integral_constant<int, 1>{});
+    float v = x[0];
+    if (n == 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, 8));
+    if (n <= 2) v = join(v, __shfl_xor_sync(0xffffffffu, v, 16));
+    return v;
 }
 
 __device__ __forceinline__ void gf_bar() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
@@ -88,32 +125,41 @@ __device__ __forceinline__ int gf_channel(int t, int at) { return (t < 4 ? 128 *
 
 __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<GaFew> walk, int warp, int lane) {
     const int quarter = warp & 3, half = warp >> 2, key = 32 * quarter + lane, tid = threadIdx.x;
-    const int c0 = 32 * half;                                      // this warp's rows
-    const uint32_t tm = sm.tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
+    const uint32_t tm0 = sm.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     GaWait wait;
-    uint32_t blk = 0, seg_no = 0;
-    GaSeg s;
-    while (walk.next(A, s)) {
-        if (s.T == 0) {
+    uint32_t blk = 0;
+    auto find = [&](GaSeg &s, uint32_t &no) {                      // the next segment with entries; no counts all
+        for (;; ++no) {
+            if (!walk.next(A, s)) return false;
+            if (s.T != 0) return true;
             ga_own_only(A, s, warp, lane);
-            ++seg_no;
-            continue;
         }
+    };
+    auto load_q = [&](const GaSeg &s) {
+        ga_load_q<kGfQSlab, 1>(A, sm.q, sm.scale, s, warp >> 1, 8 * (warp & 1), lane);
+        fence_proxy_async_smem();
+    };
+    auto reset = [&]() {
+        sm.m[tid] = -INFINITY;
+        sm.nref[tid] = kGfNone;
+    };
+    GaSeg s;
+    uint32_t seg_no = 0;
+    bool more = find(s, seg_no);
+    if (!more) return;
+    load_q(s);
+    if (tid < kGfRows) reset();
+    gf_bar();                                                      // the tile is whole
+    if (tid == 0) mbar_arrive(&sm.q_full);
+    while (more) {
         const int32_t *pages = A.page_table + static_cast<int64_t>(s.g) * A.max_pages;
         auto page_of = [&](int kb) {                               // of this thread's key, -1: it does not count
             const int pos = kb * kGfBlk + key;
             return key < kGfBlk && pos < s.T ? __ldg(pages + pos / kPage) : -1;
         };
         int page = page_of(s.k0);
-        ga_load_q<kGfQSlab, 1>(A, sm.q, sm.scale, s, warp >> 1, 8 * (warp & 1), lane);
-        if (tid < kGfRows) {
-            sm.m[tid] = -INFINITY;
-            sm.nref[tid] = kGfNone;
-        }
-        fence_proxy_async_smem();
-        gf_bar();                                                  // the tile is whole; the segment before is written
-        if (tid == 0) mbar_arrive(&sm.q_full);
-        const int live = min(max(s.ntok - 2 * half, 0), 2);        // tokens of this warp
+        const int live = s.ntok, c0 = 8 * live * half;             // this warp's rows: live x 8 from c0 on
+        const uint32_t tm = tm0 + c0;
         float2 l[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) l[i] = make_float2(0.0f, 0.0f);
@@ -137,16 +183,17 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
                     x[i + 1] = ok ? a.y : -INFINITY;
                     x[i + 2] = ok ? b.x : -INFINITY;
                     x[i + 3] = ok ? b.y : -INFINITY;
-                    if (i < 16 * live) over |= fmaxf(fmaxf(x[i], x[i + 1]), fmaxf(x[i + 2], x[i + 3])) > kGaSlack;
+                    if (i < 8 * live) over |= fmaxf(fmaxf(x[i], x[i + 1]), fmaxf(x[i + 2], x[i + 3])) > kGaSlack;
                 }
                 if (pass == 1 || !gf_any(over)) break;
                 // new references: rows' maxima over the block's keys
                 ga_tmem_ld32(tm, x);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = ok ? x[i] : -INFINITY;
-                sm.col[quarter][c0 + lane] = gf_across<true>(x, lane);
+                const float top = gf_across<true>(x, live, lane);
+                if (lane < 8 * live) sm.col[quarter][c0 + lane] = top;
                 gf_bar();
-                if (tid < kGfRows) {
+                if (tid < kHeads * live) {
                     float mx = fmaxf(fmaxf(sm.col[0][tid], sm.col[1][tid]), fmaxf(sm.col[2][tid], sm.col[3][tid]));
                     mx = mx == -INFINITY ? mx : mx * sm.scale[tid];
                     const float m = sm.m[tid];
@@ -167,44 +214,50 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
 #pragma unroll 1
                     for (int c = kGfOCol; c < kGfOCol + kGfTiles * kGfRows; c += kGfRows)
 #pragma unroll 1
-                        for (int j = 0; j < 32; j += 16) {
-                            float a[16];
-                            uint32_t o[16];
-                            tmem_ld16(tm + c + j, a);
+                        for (int j = 0; j < 8 * live; j += 8) {
+                            float a[8];
+                            gf_tmem_ld8(tm + c + j, a);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(a[i] * sm.fac[c0 + j + i]);
-                            ga_tmem_st16(tm + c + j, o);
+                            for (int i = 0; i < 8; ++i) a[i] *= sm.fac[c0 + j + i];
+                            gf_tmem_st8(tm + c + j, a);
                         }
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (j >= live) continue;
-                uint32_t p[8];
+            for (int j = 0; j < 4; ++j) {
+                if (j >= live) break;
+                uint32_t p[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 e = make_float2(ga_ex2(x[16 * j + 2 * i]), ga_ex2(x[16 * j + 2 * i + 1]));
-                    l[8 * j + i] = ga_add2(l[8 * j + i], e);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 e = make_float2(ga_ex2(x[8 * j + 2 * i]), ga_ex2(x[8 * j + 2 * i + 1]));
+                    l[4 * j + i] = ga_add2(l[4 * j + i], e);
                     p[i] = f32x2_f16x2(e.x, e.y);
                 }
-                if (key < kGfBlk) {
-                    uint4 *to = reinterpret_cast<uint4 *>(sm.p + (c0 / 8 + 2 * j) * kGfKSlab + key * 16);
-                    to[0] = make_uint4(p[0], p[1], p[2], p[3]);
-                    to[kGfKSlab / 16] = make_uint4(p[4], p[5], p[6], p[7]);
-                }
+                if (key < kGfBlk)
+                    *reinterpret_cast<uint4 *>(sm.p + (c0 / 8 + j) * kGfKSlab + key * 16) = make_uint4(p[0], p[1], p[2], p[3]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_full);
         }
-        // ---- end of the segment
+        // ---- end of the segment: the next one's queries first, so that its scores are computed meanwhile
+        GaSeg n;
+        uint32_t n_no = seg_no + 1;
+        more = find(n, n_no);
+        gf_bar();                                                  // all have read their scores and scales
+        if (more) {
+            load_q(n);
+            gf_bar();
+            if (tid == 0) mbar_arrive(&sm.q_full);
+        }
         wait(&sm.o_done, (blk - 1) & 1u);
         tc_fence_after();
         float x[32];
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[2 * i] = l[i].x, x[2 * i + 1] = l[i].y;
-        sm.col[quarter][c0 + lane] = gf_across<false>(x, lane);
+        const float part = gf_across<false>(x, live, lane);
+        if (lane < 8 * live) sm.col[quarter][c0 + lane] = part;
         gf_bar();
         const bool whole = s.k0 == 0 && s.k1 == s.blocks;
         const int64_t slot = 2 * blockIdx.x + (seg_no > 0);
@@ -223,6 +276,7 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
                 A.lse[r] = all == 0.0f ? -INFINITY : (ref + log2f(all)) * 0.6931471805599453f;
             }
         }
+        if (tid < kGfRows) reset();
         gf_bar();
 #pragma unroll 1
         for (int t = 0; t < kGfTiles; ++t) {
@@ -230,19 +284,19 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
             const int ch = gf_channel(t, 32 * quarter + lane);
 #pragma unroll 1
             for (int j = 0; j < live; ++j) {
-                const int tok = 2 * half + j;
-                float a[16];
-                tmem_ld16(tm + kGfOCol + t * kGfRows + 16 * j, a);
+                const int row = c0 + 8 * j, tok = row / kHeads, h0 = row % kHeads;
+                float a[8];
+                gf_tmem_ld8(tm + kGfOCol + t * kGfRows + 8 * j, a);
                 if (!whole) {
-                    float *po = A.part_o + (slot * A.tok_slots + tok) * (kDim * kHeads) + ch;
+                    float *po = A.part_o + ((slot * A.tok_slots + tok) * kHeads + h0) * kDim + ch;
 #pragma unroll
-                    for (int h = 0; h < kHeads; ++h) po[h * kDim] = a[h];
+                    for (int h = 0; h < 8; ++h) po[h * kDim] = a[h];
                 } else {
-                    const int64_t to = static_cast<int64_t>(s.tok0 + tok) * (kHeads * kDim) + ch;
+                    const int64_t to = (static_cast<int64_t>(s.tok0 + tok) * kHeads + h0) * kDim + ch;
 #pragma unroll
-                    for (int h = 0; h < kHeads; ++h) {
-                        float v = a[h] * sm.fac[tok * kHeads + h];
-                        const float fo = sm.own[tok * kHeads + h];
+                    for (int h = 0; h < 8; ++h) {
+                        float v = a[h] * sm.fac[row + h];
+                        const float fo = sm.own[row + h];
                         if (fo != 0.0f) v += fo * __ldg(A.o_own + to + h * kDim);
                         A.out[to + h * kDim] = __float2bfloat16_rn(v);
                     }
@@ -250,7 +304,8 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
             }
         }
         tc_fence_before();
-        ++seg_no;
+        s = n;
+        seg_no = n_no;
     }
 }
 
@@ -338,10 +393,10 @@ __device__ __forceinline__ void gf_mma(const GaArgs &A, GfSmem &sm, GaWalk<GaFew
         if (s.T == 0) continue;
         wait(&sm.q_full, tile_no & 1u);
         ++tile_no;
+        const uint32_t id_s = umma_idesc(128, kHeads * s.ntok, false, false), id_o = umma_idesc(128, kHeads * s.ntok, true, true);
         for (int kb = s.k0; kb < s.k1; ++kb, ++blk) {
             const uint32_t par = blk & 1u, acc = kb > s.k0;
-            constexpr uint32_t id_s = umma_idesc(128, kGfRows, false, false), hi = ga_desc_hi(128);
-            constexpr uint32_t id_o = umma_idesc(128, kGfRows, true, true), hi_o = ga_desc_hi(kGfKSlab);
+            constexpr uint32_t hi = ga_desc_hi(128), hi_o = ga_desc_hi(kGfKSlab);
             constexpr uint32_t da = 2 * kGfKSlab >> 4, db = 2 * kGfQSlab >> 4;          // 16 channels
             // S's columns are free: p_full of the block before has been awaited
 #pragma unroll 1
@@ -351,10 +406,10 @@ __device__ __forceinline__ void gf_mma(const GaArgs &A, GfSmem &sm, GaWalk<GaFew
 #pragma unroll 1
                 for (int c = 2 * r; c < (r < kGfRounds - 1 ? 2 * r + 2 : 9); ++c) {
                     const uint32_t a = d_k + c * (4 * da), b = d_q + c * (4 * db);
-                    ga_mma_ss<id_s, 0, hi, 0, hi>(one, 0u, a, b, c > 0);
-                    ga_mma_ss<id_s, da, hi, db, hi>(one, 0u, a, b, 1u);
-                    ga_mma_ss<id_s, 2 * da, hi, 2 * db, hi>(one, 0u, a, b, 1u);
-                    ga_mma_ss<id_s, 3 * da, hi, 3 * db, hi>(one, 0u, a, b, 1u);
+                    gf_mma_ss<0, hi, 0, hi>(one, id_s, 0u, a, b, c > 0);
+                    gf_mma_ss<da, hi, db, hi>(one, id_s, 0u, a, b, 1u);
+                    gf_mma_ss<2 * da, hi, 2 * db, hi>(one, id_s, 0u, a, b, 1u);
+                    gf_mma_ss<3 * da, hi, 3 * db, hi>(one, id_s, 0u, a, b, 1u);
                 }
             }
             ga_commit(one, &sm.s_full);
@@ -363,13 +418,13 @@ __device__ __forceinline__ void gf_mma(const GaArgs &A, GfSmem &sm, GaWalk<GaFew
 #pragma unroll 1
             for (int t = 0; t < kGfTiles; ++t) {
                 const uint32_t a = d_v + (t < 4 ? 16 * t : 56) * (kGfKSlab >> 4), d = kGfOCol + t * kGfRows;
-                ga_mma_ss<id_o, 0, hi_o, 0, hi_o>(one, d, a, d_p, acc);
-                ga_mma_ss<id_o, 16, hi_o, 16, hi_o>(one, d, a, d_p, 1u);
-                ga_mma_ss<id_o, 32, hi_o, 32, hi_o>(one, d, a, d_p, 1u);
-                ga_mma_ss<id_o, 48, hi_o, 48, hi_o>(one, d, a, d_p, 1u);
-                ga_mma_ss<id_o, 64, hi_o, 64, hi_o>(one, d, a, d_p, 1u);
-                ga_mma_ss<id_o, 80, hi_o, 80, hi_o>(one, d, a, d_p, 1u);
-                ga_mma_ss<id_o, 96, hi_o, 96, hi_o>(one, d, a, d_p, 1u);
+                gf_mma_ss<0, hi_o, 0, hi_o>(one, id_o, d, a, d_p, acc);
+                gf_mma_ss<16, hi_o, 16, hi_o>(one, id_o, d, a, d_p, 1u);
+                gf_mma_ss<32, hi_o, 32, hi_o>(one, id_o, d, a, d_p, 1u);
+                gf_mma_ss<48, hi_o, 48, hi_o>(one, id_o, d, a, d_p, 1u);
+                gf_mma_ss<64, hi_o, 64, hi_o>(one, id_o, d, a, d_p, 1u);
+                gf_mma_ss<80, hi_o, 80, hi_o>(one, id_o, d, a, d_p, 1u);
+                gf_mma_ss<96, hi_o, 96, hi_o>(one, id_o, d, a, d_p, 1u);
                 if (t < 3) ga_commit(one, &sm.k_free[t]);
             }
             ga_commit(one, &sm.k_free[kGfRounds - 1]);
@@ -397,7 +452,16 @@ group_attn_few_kernel(const GaArgs A) {
         fence_mbar_init();
     }
     pdl_wait();
-    if (!ga_begin<GaFew>(A, sm)) return;
+    ga_locate<GaFew>(A, sm);
+    __syncthreads();
+    const int64_t total = sm.total;
+    const int ranges = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+    if (blockIdx.x == 0 && tid == 0) {
+        A.plan->total = total;
+        A.plan->ranges = ranges;
+    }
+    if (static_cast<int>(blockIdx.x) >= ranges) return;
+    if (tid == 0) ga_begin<GaFew>(A, sm, total, ranges);
     if (warp == kGaMmaWarp) {
         tmem_alloc(&sm.tmem, 512);
         tmem_relinquish();
