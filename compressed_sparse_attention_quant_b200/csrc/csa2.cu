@@ -735,11 +735,16 @@ csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D, const csa2_
     A.part_ml = reinterpret_cast<float2 *>(base + ga_plan_bytes());
     A.part_o = reinterpret_cast<float *>(base + ga_plan_bytes() + ga_ml_bytes(A.tok_slots));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int ctas = std::min(dev->sm_count, kGaMaxCtas);
+    // No more ranges than there can be steps, and no more CTAs to join them than slices of tokens.
+    const int tok = A.few ? kGfTok : kGaTok, blk = A.few ? kGfBlk : kGaBlk, gap = A.few ? kGfGap : kGaGap;
+    const int64_t tiles = std::min<int64_t>(N, (N + tok - 1) / tok + G);
+    const int64_t steps = tiles * (gap + std::max<int64_t>(1, (static_cast<int64_t>(max_pages) * kPage + blk - 1) / blk));
+    const int ctas = static_cast<int>(std::min<int64_t>(std::min(dev->sm_count, kGaMaxCtas), steps));
+    const int join = static_cast<int>(std::min<int64_t>(kGmCtasPerSm * dev->sm_count, kGmSlices * static_cast<int64_t>(N)));
     const cudaError_t e = A.few ? launch_pdl(group_attn_few_kernel, dim3(ctas), dim3(kGaThreads), kGfSmemBytes, st, A)
                                 : launch_pdl(group_attn_kernel, dim3(ctas), dim3(kGaThreads), kGaSmemBytes, st, A);
     if (e != cudaSuccess) return CSA2_ERR_CUDA;
-    return cuda_status(launch_pdl(group_attn_merge_kernel, dim3(kGmCtasPerSm * ctas), dim3(kGmThreads), 0, st, A));
+    return cuda_status(launch_pdl(group_attn_merge_kernel, dim3(join), dim3(kGmThreads), 0, st, A));
 }
 
 csa2_status csa2_plan(const int *modes, int n_layers, int *kv_owner, int *index_src) {

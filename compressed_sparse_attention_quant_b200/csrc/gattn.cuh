@@ -327,13 +327,14 @@ __device__ __forceinline__ void ga_locate(const GaArgs &A, Smem &sm) {
         }
         if (lane == 31) sm.scan[warp] = incl;
         __syncthreads();
-        begin = base + incl - mine;
-#pragma unroll 1
-        for (int w = 0; w < kWarps; ++w) {
-            const int64_t v = sm.scan[w];
-            if (w < warp) begin += v;
-            base += v;
+        int64_t before = lane < kWarps ? sm.scan[lane] : 0;
+#pragma unroll
+        for (int d = 1; d < kWarps; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= d) before += o;
         }
+        begin = base + incl - mine + __shfl_sync(0xffffffffu, before, max(warp - 1, 0)) * (warp > 0);
+        base += __shfl_sync(0xffffffffu, before, kWarps - 1);
         __syncthreads();
     };
     for (int g0 = 0; g0 < A.G; g0 += kGaThreads) scan(g0, blockIdx.x == 0);

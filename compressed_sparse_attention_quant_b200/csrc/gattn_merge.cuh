@@ -15,6 +15,7 @@ namespace csa2 {
 // threads take every fourth partial each.
 constexpr int kGmThreads = 256;
 constexpr int kGmCtasPerSm = 4;
+constexpr int kGmSlices = kDim / 16;                               // 36, the most that a token is cut into
 constexpr int kGmBatch = 8;                                        // partials loaded together
 
 struct GmSmem {
@@ -164,7 +165,7 @@ group_attn_merge_kernel(const GaArgs A) {
     const int tokens = sm.before[kGaMaxCtas];
     // slices of 16 channels while 36 of them per token fit one wave of CTAs, then of 64, then of 192
     const int grid = static_cast<int>(gridDim.x);
-    const int per = tokens * 36 <= grid ? 36 : tokens * 9 <= 2 * grid ? 9 : 3;
+    const int per = tokens * kGmSlices <= grid ? kGmSlices : tokens * 9 <= 2 * grid ? 9 : 3;
     for (int unit = blockIdx.x; unit < tokens * per; unit += grid) {
         const int ut = unit / per, slice = unit - ut * per;
         int lo = 0, hi = kGaMaxCtas;                               // the boundary: before[c] <= ut < before[c + 1]
@@ -179,7 +180,7 @@ group_attn_merge_kernel(const GaArgs A) {
         const int c0 = lo - 1, n = static_cast<int>(((t.begin + t.blocks) * ranges - 1) / total) - c0 + 1;
         const int slot0 = 2 * c0 + (ga_range(total, c0, ranges) < t.begin - (A.few ? kGfGap : kGaGap) ? 1 : 0);
         const int64_t row = static_cast<int64_t>(t.tok0 + tok) * kHeads;
-        if (per == 36) gm_slice<0>(A, sm, c0, n, slot0, tok, row, slice * 16, slice == 0);
+        if (per == kGmSlices) gm_slice<0>(A, sm, c0, n, slot0, tok, row, slice * 16, slice == 0);
         else if (per == 9) gm_slice<1>(A, sm, c0, n, slot0, tok, row, slice * 64, slice == 0);
         else gm_slice<3>(A, sm, c0, n, slot0, tok, row, slice * 192, slice == 0);
     }
