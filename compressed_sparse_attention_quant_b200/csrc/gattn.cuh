@@ -1,29 +1,31 @@
-// gattn.cuh -- K12/K13: group attention over the paged FP4 cache. Every query
-// token of group g attends to the first kv_lens[g] entries of the group's
-// pages (keys = values), and the result is joined with the token's own part.
+// gattn.cuh -- K12: group attention over the paged FP4 cache. Every query token
+// of group g attends to the first kv_lens[g] entries of the group's pages
+// (keys = values), and the result is joined with the token's own part. This is
+// the form for many tokens per group; gattn_few.cuh has the one for few.
 //
-// K12 runs both products on the tensor cores (tcgen05, accumulators in tensor
+// Both products run on the tensor cores (tcgen05, accumulators in tensor
 // memory) for row tiles of 8 tokens x 16 heads = 128 rows and blocks of 64
 // keys (one page):
 //   S [128 x 64]   = Q [128 x 576] . K^T              (36 MMAs, K = 16)
-//   O [128 x 576] += P [128 x 64] . V, V = K          (4 MMAs per channel block)
-// Bound: the tensor pipe, 2,304 cycles a block at its nominal rate. What
-// decides the layout is that a row tile of 128 x 576 fp32 outputs (288 KB) is
-// more than tensor memory (256 KB), and that shared-memory traffic (Q and K
-// are read for S, V for O, and K is written once: 576 cycles each but Q's
-// 1,152) only stays below the MMA time with all 128 rows in one CTA. So the
-// first 416 channels of O accumulate in tensor memory; the other 160 come out
-// of the tensor cores block by block, 32 channels at a time, and are added up
-// in the registers of the softmax threads. Splitting the channels over two
-// CTAs would compute S twice (1.5 times the MMAs); 64 rows per CTA would read
-// and write K for half the rows.
+//   O [128 x 576] += P [128 x 64] . V, V = K          (4 MMAs per group of channels)
+// What decides the layout: a row tile of 128 x 576 fp32 outputs (288 KB) is
+// more than tensor memory (256 KB), Q (147,456 B) and one block of K
+// (73,728 B) fill shared memory, and its bandwidth (128 B a cycle) is shared
+// by the MMAs' operands and the dequantised entries. So 384 channels of O
+// accumulate in tensor memory; the other 192 come out of the tensor cores
+// block by block as pieces of 64, 32, 64 and 32 channels, two in S's columns
+// (read by then) and two in columns of their own, and are added up in the
+// registers of the softmax threads, 96 each. Splitting the channels over two
+// CTAs would compute S twice. CTA pairs (cta_group::2) with each CTA
+// dequantising half of the block took 646 us where this form takes 318 (4
+// tokens over 1M keys): a hand-off between CTAs is about 1,000 cycles against
+// 330 inside one. Dequantising every block twice, so that S of the next could
+// run during the softmax, took 7,400 cycles a block against 6,500 then.
 //
-// Shared memory holds Q (f16, 147,456 B) and one block of K (73,728 B) as
-// slabs of 8 channels (16 bytes) per row: the K-major operand layout of S and
-// the MN-major one of O, so the block is dequantised once for both. The
-// block's nine chunks of 64 channels are refilled one by one as O's MMAs
-// release them. Tensor memory: O columns 0-415, S 416-479, P (f16) 480-511;
-// the 32-channel pieces use the upper half of S, which is read by then.
+// Q and K lie as slabs of 8 channels (16 bytes) per row: the K-major operand
+// layout of S and the MN-major one of O, so a block is dequantised once for
+// both. Tensor memory: O in columns 0-383, S 384-447, pieces 448-479, P (f16)
+// 480-511.
 //   warps 0-7   load the query tile, then per block the softmax: thread = row,
 //               warps 0-3 the first 32 keys and 4-7 the others. Exp2 domain;
 //               the reference maximum rises only when a block exceeds it by
@@ -32,14 +34,26 @@
 //               Probabilities are rounded to f16 for the MMA (2^-11, below the
 //               output's bf16); their sum is taken before, in fp32. Then they
 //               add the pieces, and at the end of a row tile write it.
-//   warps 8-11  dequantise: E2M1 x E4M3 is exact in f16.
-//   warp 12     one thread issues the MMAs (warps 13-15 only fill its warpgroup).
+//   warp 8      issues the MMAs, one lane under a predicate.
+//   warps 9-14  dequantise: E2M1 x E4M3 is exact in f16. The codes of the next
+//               block are in registers while this one is multiplied, and its
+//               chunks are refilled in three rounds as O's MMAs release them.
+// The roles' loops are kept rolled where they can be: 16 warps with five kinds
+// of code press on the instruction cache (rolling the MMA loops took its misses
+// from 669K to 63K and a tenth off the time).
+//
 // The work is one flat list of (row tile, block) steps, cut into equal
 // contiguous ranges, one per CTA; a row tile that lies in several ranges is
 // left as unnormalised partials (m, l, O) that K13 joins. Lengths and offsets
-// are read on the device, so a captured call serves other lengths.
-// Every wait is an mbarrier wait with a time limit; a thread whose wait ran
-// out goes on without waiting, so that all reach the end.
+// are read on the device, so a captured call serves other lengths. Every wait
+// is an mbarrier wait with a limit; a thread whose wait ran out goes on without
+// waiting, so that all reach the end.
+//
+// Bound and measured: about 5,080 cycles a block, of which S takes 1,730 (48
+// to 64 cycles an MMA, the longer while the block is being written), the
+// softmax 1,180 in which the tensor pipe idles (512 of them the exponentials),
+// O 1,450 and the rest hand-offs. 64 tokens over 32,768 keys: 107 us, 720
+// TFLOP/s, of it some 30 us for query tiles in, partials out and K13.
 #pragma once
 
 #include "attn.cuh"
@@ -67,7 +81,7 @@ constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a 
 // A block's nine chunks are filled, multiplied and released in three rounds, in
 // the order in which O's MMAs are done with them: 2 r, 2 r + 1 and 6 + r.
 constexpr int kGaRounds = 3;
-constexpr int kGaGap = 5;
+constexpr int kGaGap = 5;                                          // 2: 93 us for 8 groups of 64 tokens, 5: 74
 constexpr float kGaSlack = 8.0f;                                   // log2 units a block may exceed the reference
 static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 96, "tensor memory is full; pieces of 64, 32, 64 and 32 channels");
 

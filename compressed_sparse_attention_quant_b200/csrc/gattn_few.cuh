@@ -20,9 +20,20 @@
 //               one of them exceeds its reference by more than 8 do all take
 //               the maxima over the keys (a transposing butterfly) and rescale.
 //               A row's sum is kept per key, 32 in registers, to the end.
-//   warp 8      issues the MMAs.
+//   warp 8      issues the MMAs, with 16 columns per token present.
 //   warps 9-15  dequantise, 16 keys each (112 = 7 x 16; 16 keys share a page).
-// The last 128 channels of O^T are 448 .. 575: 64 of them come twice.
+// The last 128 channels of O^T are 448 .. 575: 64 of them come twice. A tile's
+// last scores read, its queries make room for the next tile's, so that those
+// scores are there when the outputs have been written.
+//
+// Bound and measured: shared-memory bandwidth. With 64 columns a block moves
+// 6 KB for each of 71 MMAs, 126 KB of entries and 14 KB of P, 4,400 cycles at
+// 128 B each, and the softmax, in which nothing moves because no chunk of K is
+// free before its MMAs, adds 1,400: some 6,400 cycles for 112 keys, against
+// 5,080 for 64 in K12; with 16 columns 5,600. 4 tokens over 1M keys 261 us
+// (K12 315), 64 groups of 1 token over 4,096 keys each 74 us (K12 99.5). At 5
+// or more tokens a group takes two tiles here, and K12 wins: 32 groups of 5
+// over 4,096 keys 88 us against 70, of 4 61 against 69.
 #pragma once
 
 #include "gattn.cuh"
@@ -30,7 +41,7 @@
 namespace csa2 {
 
 constexpr int kGfTok = 4, kGfRows = kGfTok * kHeads;               // 64
-constexpr int kGfBlk = 112, kGfGap = 2;
+constexpr int kGfBlk = 112, kGfGap = 2;                            // gaps 1, 2, 3, 5: 74.9, 74.9, 77.8, 80.6 us for 64 groups of one token
 using GaFew = GaForm<kGfTok, kGfBlk, kGfGap>;
 constexpr int kGfDeqWarps = 7;
 constexpr int kGfQSlab = kGfRows * 16, kGfKSlab = kGfBlk * 16;     // 1,024 and 1,792 B

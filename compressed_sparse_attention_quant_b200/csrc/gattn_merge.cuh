@@ -6,13 +6,16 @@
 namespace csa2 {
 
 // ------------------------------------------------------------------ K13
-// Joins the partials of the row tiles that K12's ranges cut, with the own
-// part. Memory-bound in principle (36,864 B per partial and token, L2), latency
-// bound per unit of work, so a unit is one slice of a token's channels: all
-// 192, 64 or 16 of them, the smaller the fewer tokens there are to fill the
-// GPU, and the first partials are loaded together with the maxima and sums. A
-// thread takes 4 channels of a head; with 16 channels the four groups of 64
-// threads take every fourth partial each.
+// Joins the partials of the row tiles that the ranges cut, with the own part:
+// with M the largest m, out = (sum_p 2^(m_p - M) O_p + 2^(own - M) o_own) / L,
+// L = sum_p 2^(m_p - M) l_p + 2^(own - M), lse = M + log L. Memory-bound in
+// principle (36,864 B per partial and token, from L2: 47 MB for 64 tokens over
+// 32,768 keys, about 12 us), latency-bound per unit of work. So a unit is a
+// slice of a token's channels, 192, 64 or 16 of them, the smaller the fewer
+// tokens there are to fill the GPU, and the first partials are loaded together
+// with the maxima and sums. A thread takes 4 channels of a head; with 16
+// channels the four groups of 64 threads take every fourth partial each. The
+// order of the additions is fixed: a call gives the same bits again.
 constexpr int kGmThreads = 256;
 constexpr int kGmCtasPerSm = 4;
 constexpr int kGmSlices = kDim / 16;                               // 36, the most that a token is cut into

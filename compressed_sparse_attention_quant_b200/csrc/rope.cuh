@@ -57,6 +57,13 @@ struct RopeArgs {
 // rotated by the same frequencies. Then a lane quantises one 16-channel group
 // of each token, and of the last step, with four groups and the key of every
 // token left, 16 lanes take the groups and 16 the keys, 4 lanes per key.
+//
+// Bound and measured: 128K tokens with keys take 83 us, the HBM floor being 34
+// (220 MB at the copy rate) and the instructions' 51 (456 a token at full
+// issue, 148 of them for the 32 angles and pairs). A CTA of 8 tokens with a
+// barrier between rotation and quantisation took 127; the same as a loop over
+// resident CTAs, with the next rows on the way, 275: its one warp of keys held
+// up the other nine. 64 tokens: 3.9 us from launch to launch.
 constexpr int kApTok = 4;
 constexpr int kApWarps = 4;
 constexpr int kApThreads = 32 * kApWarps;
@@ -264,6 +271,10 @@ inline cudaError_t launch_append_kv_rope(AppendArgs A, int sm_count, cudaStream_
 // angles are computed; otherwise it goes pair by pair. The other channels are
 // copied, to another tensor only, before the angles. A token's heads are shared
 // out over CTAs while there are fewer CTAs than the GPU holds.
+//
+// Measured: 64 tokens of 16 x 576 channels 2.9 us from launch to launch, 16,384
+// tokens of 4 x 64 about 8 us (2.6 by the bytes; two waves of CTAs whose time
+// is the angles' and the fence's latency).
 constexpr int kRrThreads = 256;
 constexpr int kRrTokens = 8;
 constexpr int kRrPairs = 320;                                     // angles held by a CTA (dim / 2 <= 288)
