@@ -52,7 +52,7 @@
 // Bound and measured: about 5,080 cycles a block, of which S takes 1,730 (48
 // to 64 cycles an MMA, the longer while the block is being written), the
 // softmax 1,180 in which the tensor pipe idles (512 of them the exponentials),
-// O 1,450 and the rest hand-offs. 64 tokens over 32,768 keys: 107 us, 720
+// O 1,450 and the rest hand-offs. 64 tokens over 32,768 keys: 106 us, 730
 // TFLOP/s, of it some 30 us for query tiles in, partials out and K13.
 #pragma once
 
@@ -121,8 +121,12 @@ struct GaPlan {
     struct Tile { int64_t begin; int blocks, tok0, ntok; } first[kGaMaxCtas];
 };
 
-// First step of range c.
-__device__ __forceinline__ int64_t ga_range(int64_t total, int c, int ranges) { return total * c / ranges; }
+// First step of range c (a 64-bit division only where 32 bits do not hold the product).
+__device__ __forceinline__ int64_t ga_range(int64_t total, int c, int ranges) {
+    if (total <= 0xffffffffll / kGaMaxCtas)
+        return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ranges);
+    return total * c / ranges;
+}
 
 struct GaGroup { int tok0, n, T, blocks; };
 
