@@ -123,3 +123,23 @@ def test_two_graphs_in_turn(lib):
     for (ref, ref_lse), r in zip(refs, runs):
         assert torch.equal(ref, r[1]) and torch.equal(ref_lse, r[2])
     assert lib.last_device_error() == 0
+
+
+def test_no_group_has_tokens(lib):
+    c = Case(lib, [0, 0, 0], [100, 0, 70], before=2, after=3).with_own()
+    out = torch.full((c.N, H, DIM), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.N, H), -2.0, device="cuda")
+    for _ in range(2):
+        c.call(out, lse)
+    assert lib.last_device_error() == 0
+    assert (out == 3.0).all() and (lse == -2.0).all()
+
+
+def test_most_groups(lib):
+    tokens, lens = [0] * 65535, [0] * 65535
+    for g, (t, n) in {0: (1, 65), 511: (2, 300), 512: (1, 1), 40000: (7, 1000), 65534: (1, 64)}.items():
+        tokens[g], lens[g] = t, n
+    c = Case(lib, tokens, lens, seed=26).with_own()
+    out, lse = c.call()
+    assert lib.last_device_error() == 0
+    c.check(out, lse)
