@@ -1,7 +1,8 @@
 // csa2.cu -- C-ABI entry points of the CSA2 FP4 sparse-decode library:
 // argument validation, workspace layout and kernel launches. The kernels are
 // in quant.cuh (K1), indexer.cuh (K2), topk.cuh (K3), attn.cuh (K4/K5),
-// pool.cuh (K6), replay.cuh (K9), rope.cuh (K10/K11) and gattn.cuh (K12/K13).
+// pool.cuh (K6), replay.cuh (K9), rope.cuh (K10/K11), gattn.cuh
+// and gattn_few.cuh (K12) and gattn_merge.cuh (K13).
 #include <cmath>
 #include <cstdint>
 #include <cstring>

@@ -808,7 +808,10 @@ __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk<GaWid
             // 400 cycles of other MMAs lie between a piece and the next use of its columns
 #pragma unroll 1
             for (uint32_t h = 0; h < 2; ++h) {
-                if (h > 0) wait(&sm.ds_empty, 0u);
+                if (h > 0) {
+                    wait(&sm.ds_empty, 0u);
+                    tc_fence_after();
+                }
                 ga_pv<64>(one, kGaSCol, d_v + 6 * dv + h * (3 * dv / 2), 0u);
                 ga_commit(one, &sm.ds_full);
                 wait(&sm.dd_empty, h ^ 1u);
