@@ -201,9 +201,10 @@ struct GaSmem {
     uint64_t q_full;                   // query tile in
     uint64_t s_full;                   // scores in tensor memory
     uint64_t p_full;                   // probabilities in tensor memory, O rescaled
-    uint64_t ds_full, ds_empty;        // a piece in S's columns; read
-    uint64_t dd_full, dd_empty;        // a piece in its own 32 columns; read
-    uint64_t o_done;                   // a block's O is complete
+    uint64_t ds_full, ds_empty;        // a piece in S's columns; the first one read
+    uint64_t dd_full, dd_empty;        // a piece in its own 32 columns; the first one read
+    // A round's chunks: in (the first round's also says that S's columns are free), and multiplied (the last
+    // round's also says that the block's O is complete).
     uint64_t k_full[kGaRounds], k_free[kGaRounds];
     uint32_t tmem;
     float scale[kGaRows];              // a row's softmax scale (log2) times its query exponent
@@ -497,6 +498,7 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk<G
     GaWait wait;
     uint32_t blk = 0, seg_no = 0;
     GaSeg s;
+    if (lane == 0) mbar_arrive(&sm.k_full[0]);                     // S's columns are free for the first block
     while (walk.next(A, s)) {
         if (s.T == 0) {
             ga_own_only(A, s, warp, lane);
@@ -523,7 +525,7 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk<G
             for (int c = 0; c < kN; c += 16) {
                 float a[16];
                 tmem_ld16(tm + col + kN * half + c, a);
-                if (c + 16 == kN) {                                // the columns are free
+                if (c + 16 == kN && empty != nullptr) {            // the columns are free
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(empty);
@@ -596,11 +598,11 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk<G
             l += sum.x + sum.y;
             piece_add(std::integral_constant<int, 32>{}, 0, &sm.ds_full, &sm.ds_empty, kGaSCol, 0u);
             piece_add(std::integral_constant<int, 16>{}, 32, &sm.dd_full, &sm.dd_empty, kGaDCol, 0u);
-            piece_add(std::integral_constant<int, 32>{}, 48, &sm.ds_full, &sm.ds_empty, kGaSCol, 1u);
-            piece_add(std::integral_constant<int, 16>{}, 80, &sm.dd_full, &sm.dd_empty, kGaDCol, 1u);
+            piece_add(std::integral_constant<int, 32>{}, 48, &sm.ds_full, &sm.k_full[0], kGaSCol, 1u);
+            piece_add(std::integral_constant<int, 16>{}, 80, &sm.dd_full, nullptr, kGaDCol, 1u);   // p_full says it next
         }
         // ---- end of the segment
-        wait(&sm.o_done, (blk - 1) & 1u);
+        wait(&sm.k_free[kGaRounds - 1], (blk - 1) & 1u);
         tc_fence_after();
         const int tok = row >> 4, h = row & 15;
         const bool live = tok < s.ntok;
@@ -786,11 +788,10 @@ __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk<GaWid
             const uint32_t par = blk & 1u, acc = kb > s.k0;
             constexpr uint32_t id = umma_idesc(kGaRows, kGaBlk, false, false), hi = ga_desc_hi(128);
             constexpr uint32_t da = 2 * kGaQSlab >> 4, db = 2 * kGaKSlab >> 4, dv = 8 * kGaKSlab >> 4;   // 16, 16 and 64 channels
-            wait(&sm.ds_empty, 1u);                                // S's columns: the last piece there has been read
-            tc_fence_after();
 #pragma unroll 1
             for (int r = 0; r < kGaRounds; ++r) {
                 wait(&sm.k_full[r], par);
+                tc_fence_after();                                  // S's columns have been read
 #pragma unroll 1
                 for (int j = 0; j < 3; ++j) {
                     const int c = j < 2 ? 2 * r + j : 6 + r;
@@ -809,13 +810,15 @@ __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk<GaWid
 #pragma unroll 1
             for (uint32_t h = 0; h < 2; ++h) {
                 if (h > 0) {
-                    wait(&sm.ds_empty, 0u);
+                    wait(&sm.ds_empty, par);
                     tc_fence_after();
                 }
                 ga_pv<64>(one, kGaSCol, d_v + 6 * dv + h * (3 * dv / 2), 0u);
                 ga_commit(one, &sm.ds_full);
-                wait(&sm.dd_empty, h ^ 1u);
-                tc_fence_after();
+                if (h > 0) {                                       // the first one: p_full said that it is free
+                    wait(&sm.dd_empty, par);
+                    tc_fence_after();
+                }
                 ga_pv<32>(one, kGaDCol, d_v + 7 * dv + h * (3 * dv / 2), 0u);
                 ga_commit(one, &sm.dd_full);
                 ga_pv<128>(one, 128 * h, d_v + h * (2 * dv), acc);
@@ -823,11 +826,10 @@ __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk<GaWid
             }
             ga_pv<128>(one, 256, d_v + 4 * dv, acc);
             ga_commit(one, &sm.k_free[2]);                         // 4, 5 and 8
-            ga_commit(one, &sm.o_done);
         }
     }
     // every MMA of this CTA is done before tensor memory goes back
-    if (blk > 0) wait(&sm.o_done, (blk - 1) & 1u);
+    if (blk > 0) wait(&sm.k_free[kGaRounds - 1], (blk - 1) & 1u);
 }
 
 __global__ void __launch_bounds__(kGaThreads, 1)
@@ -843,9 +845,8 @@ group_attn_kernel(const GaArgs A) {
         mbar_init(&sm.ds_empty, kGaSoftWarps);
         mbar_init(&sm.dd_full, 1);
         mbar_init(&sm.dd_empty, kGaSoftWarps);
-        mbar_init(&sm.o_done, 1);
         for (int i = 0; i < kGaRounds; ++i) {
-            mbar_init(&sm.k_full[i], kGaDeqWarps);
+            mbar_init(&sm.k_full[i], i == 0 ? kGaDeqWarps + kGaSoftWarps : kGaDeqWarps);
             mbar_init(&sm.k_free[i], 1);
         }
         fence_mbar_init();
