@@ -49,11 +49,11 @@
 // is an mbarrier wait with a limit; a thread whose wait ran out goes on without
 // waiting, so that all reach the end.
 //
-// Bound and measured: about 5,080 cycles a block, of which S takes 1,730 (48
-// to 64 cycles an MMA, the longer while the block is being written), the
-// softmax 1,180 in which the tensor pipe idles (512 of them the exponentials),
-// O 1,450 and the rest hand-offs. 64 tokens over 32,768 keys: 106 us, 730
-// TFLOP/s, of it some 30 us for query tiles in, partials out and K13.
+// Bound and measured: about 4,950 cycles a block, of which S takes 2,150 (60
+// an MMA: its 6 KB of operands are 48 cycles of shared memory, and the block is
+// being written meanwhile), the softmax 1,100 in which the tensor pipe idles
+// (512 of them the exponentials), O 1,300 and the rest hand-offs. 64 tokens
+// over 32,768 keys: 103 us, 750 TFLOP/s, of it some 30 us for query tiles in, partials out and K13.
 #pragma once
 
 #include "attn.cuh"

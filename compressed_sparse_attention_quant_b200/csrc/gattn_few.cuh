@@ -30,7 +30,7 @@
 // 6 KB for each of 71 MMAs, 126 KB of entries and 14 KB of P, 4,400 cycles at
 // 128 B each, and the softmax, in which nothing moves because no chunk of K is
 // free before its MMAs, adds 1,400: some 6,400 cycles for 112 keys, against
-// 5,080 for 64 in K12; with 16 columns 5,600. 4 tokens over 1M keys 261 us
+// 4,950 for 64 in K12; with 16 columns 5,600. 4 tokens over 1M keys 261 us
 // (K12 315), 64 groups of 1 token over 4,096 keys each 74 us (K12 99.5). At 5
 // or more tokens a group takes two tiles here, and K12 wins: 32 groups of 5
 // over 4,096 keys 88 us against 70, of 4 61 against 69.

@@ -266,17 +266,19 @@ inline cudaError_t launch_append_kv_rope(AppendArgs A, int sm_count, cudaStream_
 // Query rows [n][heads][dim], in place or to another tensor. A token's angles
 // serve all its heads, so a CTA computes them once for the tokens and heads it
 // takes. Where the rotated range and the distance within a pair are multiples
-// of 8 channels a thread loads 16 bytes (two of them when the row is split in
-// halves) and turns 4 or 8 pairs, and the first load is in flight while the
-// angles are computed; otherwise it goes pair by pair. The other channels are
+// of 8 channels a thread turns 4 pairs at a time, 16 bytes or (when the row is
+// split in halves) twice 8, and the first load is in flight while the angles
+// are computed; otherwise it goes pair by pair. The other channels are
 // copied, to another tensor only, before the angles. A token's heads are shared
 // out over CTAs while there are fewer CTAs than the GPU holds.
 //
 // Measured: 64 tokens of 16 x 576 channels 2.9 us from launch to launch, 16,384
-// tokens of 4 x 64 about 8 us (2.6 by the bytes; two waves of CTAs whose time
-// is the angles' and the fence's latency).
+// tokens 134 us (93 by the bytes) and of 4 x 64 channels 9.8 us (2.6 by the
+// bytes: three waves of CTAs whose time is the latency of angles and fence, and
+// the conversions to and from binary64, four per pair).
 constexpr int kRrThreads = 256;
 constexpr int kRrTokens = 8;
+constexpr int kRrCtasPerSm = 6;                                   // 128K tokens of 4 x 64 channels: 5 72 us, 6 67, 8 63 but 64 tokens 3.3 against 2.9
 constexpr int kRrPairs = 320;                                     // angles held by a CTA (dim / 2 <= 288)
 
 struct RopeRowsArgs {
@@ -290,7 +292,7 @@ struct RopeRowsArgs {
 };
 
 template <bool kWide>
-__global__ void __launch_bounds__(kRrThreads)
+__global__ void __launch_bounds__(kRrThreads, kRrCtasPerSm)
 rope_rows_kernel(const RopeRowsArgs A) {
     __shared__ double2 s_cs[kRrPairs];                            // (cos, sin) of (token, pair)
     __shared__ bool s_ok[kRrTokens];
@@ -307,23 +309,25 @@ rope_rows_kernel(const RopeRowsArgs A) {
         if (!s_ok[tid]) flag_status(kStatusBounds);
     }
     // this thread's first 16 bytes of rotated channels, or first pair
-    const int per_row = !kWide ? half : A.rope.interleaved ? half / 4 : half / 8, items = nt * nh * per_row;
-    uint4 va, vb;
+    const int per_row = kWide ? half / 4 : half, items = nt * nh * per_row;
+    uint4 v;                                                      // 4 pairs, or one
     int t = 0, i = 0;
     int64_t from = 0, to = 0;
     auto load = [&](int p) {
         const int r = p / per_row, h = r % nh;
         t = r / nh;
         i = p - r * per_row;
-        const int c = h * A.dim + (kWide ? lo + 8 * i : A.rope.first(i));
+        const int c = h * A.dim + (kWide ? lo + (A.rope.interleaved ? 8 : 4) * i : A.rope.first(i));
         from = t * A.x_stride + c;
         to = t * A.out_stride + c;
-        if (kWide) {
-            va = *reinterpret_cast<const uint4 *>(x + from);
-            if (!A.rope.interleaved) vb = *reinterpret_cast<const uint4 *>(x + from + half);
+        if (!kWide) {
+            v.x = x[from];
+            v.y = x[from + A.rope.step()];
+        } else if (A.rope.interleaved) {
+            v = *reinterpret_cast<const uint4 *>(x + from);
         } else {
-            va.x = x[from];
-            vb.x = x[from + A.rope.step()];
+            const uint2 a = *reinterpret_cast<const uint2 *>(x + from), b = *reinterpret_cast<const uint2 *>(x + from + half);
+            v = make_uint4(a.x, a.y, b.x, b.y);
         }
     };
     if (tid < items) load(tid);
@@ -360,30 +364,30 @@ rope_rows_kernel(const RopeRowsArgs A) {
     for (int p = tid; p < items; p += kRrThreads) {
         if (p != tid) load(p);
         if (!s_ok[t]) continue;
-        const double2 *cs = s_cs + t * half;
+        const double2 *cs = s_cs + t * half + (kWide ? 4 * i : i);
         if (!kWide) {
-            const uint32_t v = rope_pair(static_cast<uint16_t>(va.x), static_cast<uint16_t>(vb.x), cs[i].y, cs[i].x);
-            out[to] = static_cast<uint16_t>(v);
-            out[to + A.rope.step()] = static_cast<uint16_t>(v >> 16);
+            const uint32_t w = rope_pair(static_cast<uint16_t>(v.x), static_cast<uint16_t>(v.y), cs[0].y, cs[0].x);
+            out[to] = static_cast<uint16_t>(w);
+            out[to + A.rope.step()] = static_cast<uint16_t>(w >> 16);
         } else if (A.rope.interleaved) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                uint32_t &w = (&va.x)[e];
-                w = rope_pair(static_cast<uint16_t>(w), static_cast<uint16_t>(w >> 16), cs[4 * i + e].y, cs[4 * i + e].x);
+                uint32_t &w = (&v.x)[e];
+                w = rope_pair(static_cast<uint16_t>(w), static_cast<uint16_t>(w >> 16), cs[e].y, cs[e].x);
             }
-            *reinterpret_cast<uint4 *>(out + to) = va;
+            *reinterpret_cast<uint4 *>(out + to) = v;
         } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t &a = (&va.x)[e], &b = (&vb.x)[e];
-                const double2 c0 = cs[8 * i + 2 * e], c1 = cs[8 * i + 2 * e + 1];
+            for (int e = 0; e < 2; ++e) {
+                uint32_t &a = (&v.x)[e], &b = (&v.x)[2 + e];
+                const double2 c0 = cs[2 * e], c1 = cs[2 * e + 1];
                 const uint32_t v0 = rope_pair(static_cast<uint16_t>(a), static_cast<uint16_t>(b), c0.y, c0.x);
                 const uint32_t v1 = rope_pair(static_cast<uint16_t>(a >> 16), static_cast<uint16_t>(b >> 16), c1.y, c1.x);
                 a = __byte_perm(v0, v1, 0x5410);
                 b = __byte_perm(v0, v1, 0x7632);
             }
-            *reinterpret_cast<uint4 *>(out + to) = va;
-            *reinterpret_cast<uint4 *>(out + to + half) = vb;
+            *reinterpret_cast<uint2 *>(out + to) = make_uint2(v.x, v.y);
+            *reinterpret_cast<uint2 *>(out + to + half) = make_uint2(v.z, v.w);
         }
     }
     __threadfence();
