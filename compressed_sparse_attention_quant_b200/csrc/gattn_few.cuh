@@ -56,8 +56,8 @@ struct GfSmem {
     alignas(1024) uint8_t q[kGfRows * kDim * 2];
     alignas(1024) uint8_t k[kGfBlk * kDim * 2];
     alignas(16) uint8_t p[kGfRows * kGfBlk * 2];                   // behind k: S's unused rows read its first bytes
-    uint64_t q_full, s_full, p_full, o_done;
-    uint64_t k_full[kGfRounds], k_free[kGfRounds];
+    uint64_t q_full, s_full, p_full;
+    uint64_t k_full[kGfRounds], k_free[kGfRounds];                 // the last round's free: the block's O is complete too
     uint32_t tmem;
     alignas(16) float scale[kGfRows];                              // of a row: softmax scale (log2) times query exponent
     alignas(16) float nref[kGfRows];                               // minus its reference
@@ -262,7 +262,7 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
             gf_bar();
             if (tid == 0) mbar_arrive(&sm.q_full);
         }
-        wait(&sm.o_done, (blk - 1) & 1u);
+        wait(&sm.k_free[kGfRounds - 1], (blk - 1) & 1u);
         tc_fence_after();
         float x[32];
 #pragma unroll
@@ -439,11 +439,10 @@ __device__ __forceinline__ void gf_mma(const GaArgs &A, GfSmem &sm, GaWalk<GaFew
                 if (t < 3) ga_commit(one, &sm.k_free[t]);
             }
             ga_commit(one, &sm.k_free[kGfRounds - 1]);
-            ga_commit(one, &sm.o_done);
         }
     }
     // every MMA of this CTA is done before tensor memory goes back
-    if (blk > 0) wait(&sm.o_done, (blk - 1) & 1u);
+    if (blk > 0) wait(&sm.k_free[kGfRounds - 1], (blk - 1) & 1u);
 }
 
 __global__ void __launch_bounds__(kGaThreads, 1)
@@ -455,7 +454,6 @@ group_attn_few_kernel(const GaArgs A) {
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.s_full, 1);
         mbar_init(&sm.p_full, kGaSoftWarps);
-        mbar_init(&sm.o_done, 1);
         for (int i = 0; i < kGfRounds; ++i) {
             mbar_init(&sm.k_full[i], kGfDeqWarps);
             mbar_init(&sm.k_free[i], 1);

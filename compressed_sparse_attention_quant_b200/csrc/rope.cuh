@@ -58,16 +58,17 @@ struct RopeArgs {
 // of each token, and of the last step, with four groups and the key of every
 // token left, 16 lanes take the groups and 16 the keys, 4 lanes per key.
 //
-// Bound and measured: 128K tokens with keys take 83 us, the HBM floor being 34
+// Bound and measured: 128K tokens with keys take 77 us, the HBM floor being 34
 // (220 MB at the copy rate) and the instructions' 51 (456 a token at full
 // issue, 148 of them for the 32 angles and pairs). A CTA of 8 tokens with a
 // barrier between rotation and quantisation took 127; the same as a loop over
 // resident CTAs, with the next rows on the way, 275: its one warp of keys held
-// up the other nine. 64 tokens: 3.9 us from launch to launch.
+// up the other nine. 4, 5, 6 and 7 CTAs per SM: 94, 83, 77 and 80 us (spills).
+// 64 tokens: 3.9 us from launch to launch.
 constexpr int kApTok = 4;
 constexpr int kApWarps = 4;
 constexpr int kApThreads = 32 * kApWarps;
-constexpr int kApCtasPerSm = 5;
+constexpr int kApCtasPerSm = 6;
 
 struct AppendArgs {
     const uint16_t *x;                 // [n][x_stride] bf16

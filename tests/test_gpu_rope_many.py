@@ -10,7 +10,7 @@ from test_gpu_rope import DIM, KD, PAGE, fill, freqs, held, lib, rotate, slots_o
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("n", [5921, 8883, 11841, 12001])
+@pytest.mark.parametrize("n", [5921, 8883, 11841, 12001, 14209, 15003])
 @pytest.mark.parametrize("keys", [False, True])
 def test_append_many(lib, n, keys):
     g = torch.Generator().manual_seed(n)
