@@ -442,19 +442,31 @@ __device__ __forceinline__ void ga_load_q(const GaArgs &A, uint8_t *tile, float 
     }
 }
 
-// A segment of a group without entries: its tokens' own parts, or zeros.
+// A segment of a group without entries: its tokens' own parts, or zeros, a
+// token per warp, the loads of kAtOnce heads in flight (with one load at a time a tile
+// took 26 us, 45 with the own parts in DRAM: longer than the other ranges, and
+// 72 us instead of 50 for six groups of which one is empty).
+template <int kAtOnce>
 __device__ __forceinline__ void ga_own_only(const GaArgs &A, const GaSeg &s, int tok, int lane) {
     if (tok >= s.ntok) return;
+    const int64_t r0 = static_cast<int64_t>(s.tok0 + tok) * kHeads;
 #pragma unroll 1
-    for (int h = 0; h < kHeads; ++h) {
-        const int64_t r = static_cast<int64_t>(s.tok0 + tok) * kHeads + h;
-        const float own = A.lse_own ? __ldg(A.lse_own + r) : -INFINITY;
-        if (lane == 0) A.lse[r] = own;
-        for (int c = lane * 2; c < kDim; c += 64) {
-            float2 v = make_float2(0.0f, 0.0f);
-            if (own != -INFINITY) v = __ldg(reinterpret_cast<const float2 *>(A.o_own + r * kDim + c));
-            *reinterpret_cast<__nv_bfloat162 *>(A.out + r * kDim + c) = __floats2bfloat162_rn(v.x, v.y);
+    for (int h = 0; h < kHeads; h += kAtOnce) {
+        const int64_t r = r0 + h;
+        float2 v[9 * kAtOnce];
+        float own[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < 9 * kAtOnce; ++u)
+            v[u] = A.o_own ? __ldg(reinterpret_cast<const float2 *>(A.o_own + r * kDim) + lane + 32 * u) : make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            own[u] = A.lse_own ? __ldg(A.lse_own + r + u) : -INFINITY;
+            if (lane == 0) A.lse[r + u] = own[u];
         }
+#pragma unroll
+        for (int u = 0; u < 9 * kAtOnce; ++u)
+            reinterpret_cast<__nv_bfloat162 *>(A.out + r * kDim)[lane + 32 * u] =
+                own[u / 9] != -INFINITY ? __floats2bfloat162_rn(v[u].x, v[u].y) : __floats2bfloat162_rn(0.0f, 0.0f);
     }
 }
 
@@ -501,7 +513,7 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk<G
     if (lane == 0) mbar_arrive(&sm.k_full[0]);                     // S's columns are free for the first block
     while (walk.next(A, s)) {
         if (s.T == 0) {
-            ga_own_only(A, s, warp, lane);
+            ga_own_only<4>(A, s, warp, lane);
             ++seg_no;
             continue;
         }

@@ -143,7 +143,7 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
         for (;; ++no) {
             if (!walk.next(A, s)) return false;
             if (s.T != 0) return true;
-            ga_own_only(A, s, warp, lane);
+            ga_own_only<1>(A, s, warp, lane);                      // 2 and 4: 1 and 2% off every call, for the code alone
         }
     };
     auto load_q = [&](const GaSeg &s) {
