@@ -28,12 +28,18 @@
 // 480-511.
 //   warps 0-7   load the query tile, then per block the softmax: thread = row,
 //               warps 0-3 the first 32 keys and 4-7 the others. Exp2 domain;
-//               the reference maximum rises only when a block exceeds it by
-//               more than 8 (O is rescaled then), otherwise probabilities up
-//               to 2^8 stay as they are, at the same relative precision.
-//               Probabilities are rounded to f16 for the MMA (2^-11, below the
-//               output's bf16); their sum is taken before, in fp32. Then they
-//               add the pieces, and at the end of a row tile write it.
+//               a row's reference is its maximum at some block minus kGaHead,
+//               and rises only when a block exceeds that maximum by more than
+//               kGaSlack (O is rescaled then). So a probability is 2^kGaHead
+//               and at most 2^15 where it is largest, and f16, to which it is
+//               rounded for the MMA, has its full 2^-11 (below the output's
+//               bf16) down to 2^(-14 - kGaHead) of the largest one and steps of
+//               2^(-24 - kGaHead) below: a flat tail of T entries behind one
+//               dominant entry is off by at most T 2^(-25 - kGaHead) of its
+//               values. With the largest one at 2^0 a million entries 17.4
+//               below a sink were lost, 3% of the output. The sums are taken
+//               before, in fp32. Then they add the pieces, and at the end of a
+//               row tile write it.
 //   warp 8      issues the MMAs, one lane under a predicate.
 //   warps 9-14  dequantise: E2M1 x E4M3 is exact in f16. The codes of the next
 //               block are in registers while this one is multiplied, and its
@@ -82,7 +88,9 @@ constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a 
 // the order in which O's MMAs are done with them: 2 r, 2 r + 1 and 6 + r.
 constexpr int kGaRounds = 3;
 constexpr int kGaGap = 5;                                          // 2: 93 us for 8 groups of 64 tokens, 5: 74
-constexpr float kGaSlack = 8.0f;                                   // log2 units a block may exceed the reference
+// log2 units: what a probability of the maximum is raised by, and a block may exceed that maximum by; f16 ends below 2^16.
+constexpr float kGaHead = 7.0f, kGaSlack = 8.0f;                   // 11 and 4: 4 tokens x 1M entries of wide scores 322 us against 274
+static_assert(kGaHead + kGaSlack <= 15.0f, "probabilities stay finite in f16");
 static_assert(kGaPCol + kGaBlk / 2 == 512 && kGaRegs == 96, "tensor memory is full; pieces of 64, 32, 64 and 32 channels");
 
 // A row tile of kT tokens, blocks of kB keys, and what a row tile costs beside
@@ -108,7 +116,7 @@ struct GaArgs {
     struct GaPlan *plan;
     // [2 * ranges][tok_slots][144][16][4], 4 channels of 16 heads together; with few tokens [..][16][576]
     float *part_o;
-    float2 *part_ml;                   // [2 * ranges][tok_slots * 16]: (m in the log2 domain, l)
+    float2 *part_ml;                   // [2 * ranges][tok_slots * 16]: (the reference m in the log2 domain, l)
     int tok_slots;                     // min(8, N), with few tokens min(4, N)
     int few;                           // the form for few tokens per group
 };
@@ -583,10 +591,10 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk<G
                 ga_pair_bar(pair_bar);
                 mx = fmaxf(mx, sm.mx[par][half ^ 1][row]);
                 mx = mx == -INFINITY ? mx : mx * scale;
-                const bool raise = mx > m + kGaSlack || (m == -INFINITY && mx > m);
+                const bool raise = mx > m + (kGaHead + kGaSlack) || (m == -INFINITY && mx > m);
                 if (!__any_sync(0xffffffffu, raise)) break;
-                const float f = raise ? ga_ex2(m - mx) : 1.0f;     // 0 for the first keys of a row
-                if (raise) m = mx;
+                const float f = raise ? ga_ex2(m - (mx - kGaHead)) : 1.0f;   // 0 for the first keys of a row
+                if (raise) m = mx - kGaHead;
                 l *= f;
 #pragma unroll
                 for (int i = 0; i < kGaRegs / 2; ++i) acc[i] = make_float2(acc[i].x * f, acc[i].y * f);

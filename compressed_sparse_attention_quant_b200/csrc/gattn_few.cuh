@@ -16,9 +16,10 @@
 //   warps 0-7   load the query tile, then per block the softmax: thread = key,
 //               warps 0-3 the first half of the rows and 4-7 the other. A thread
 //               does not see a row's other keys, and does not have to: it
-//               compares its scores with the rows' references, and only when
-//               one of them exceeds its reference by more than 8 do all take
-//               the maxima over the keys (a transposing butterfly) and rescale.
+//               compares its scores with the rows' references (K12's), and only
+//               when one of them exceeds its row's maximum so far by more than
+//               kGaSlack do all take the maxima over the keys (a transposing
+//               butterfly) and rescale.
 //               A row's sum is kept per key, 32 in registers, to the end.
 //   warp 8      issues the MMAs, with 16 columns per token present.
 //   warps 9-15  dequantise, 16 keys each (112 = 7 x 16; 16 keys share a page).
@@ -62,7 +63,7 @@ struct GfSmem {
     alignas(16) float scale[kGfRows];                              // of a row: softmax scale (log2) times query exponent
     alignas(16) float nref[kGfRows];                               // minus its reference
     alignas(16) float fac[kGfRows], own[kGfRows];                  // factors of a rescaling, or of the entries and the own part
-    float m[kGfRows];
+    float m[kGfRows];                                              // its reference, -inf without keys yet
     float col[4][kGfRows];                                         // a row's maximum or sum in each quarter of the keys
     int64_t scan[kGaThreads / 32], start, total;
     int start_g;
@@ -194,7 +195,7 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
                     x[i + 1] = ok ? a.y : -INFINITY;
                     x[i + 2] = ok ? b.x : -INFINITY;
                     x[i + 3] = ok ? b.y : -INFINITY;
-                    if (i < 8 * live) over |= fmaxf(fmaxf(x[i], x[i + 1]), fmaxf(x[i + 2], x[i + 3])) > kGaSlack;
+                    if (i < 8 * live) over |= fmaxf(fmaxf(x[i], x[i + 1]), fmaxf(x[i + 2], x[i + 3])) > kGaHead + kGaSlack;
                 }
                 if (pass == 1 || !gf_any(over)) break;
                 // new references: rows' maxima over the block's keys
@@ -208,7 +209,8 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
                     float mx = fmaxf(fmaxf(sm.col[0][tid], sm.col[1][tid]), fmaxf(sm.col[2][tid], sm.col[3][tid]));
                     mx = mx == -INFINITY ? mx : mx * sm.scale[tid];
                     const float m = sm.m[tid];
-                    const bool raise = mx > m + kGaSlack || (m == -INFINITY && mx > m);
+                        const bool raise = mx > m + (kGaHead + kGaSlack) || (m == -INFINITY && mx > m);
+                    mx -= kGaHead;
                     sm.fac[tid] = raise ? ga_ex2(m - mx) : 1.0f;   // 0 for the first keys of a row
                     if (raise) {
                         sm.m[tid] = mx;
