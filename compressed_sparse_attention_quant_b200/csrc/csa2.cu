@@ -78,12 +78,14 @@ cudaError_t device_info(DeviceInfo **out) {
         e = cudaFuncSetAttribute(swa_replay_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(kRpSmemBytes));
         if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(group_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kGaSmemBytes));
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(group_attn_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kGfSmemBytes));
-        if (e != cudaSuccess) return e;
+        for (const auto kf : {group_attn_kernel<false>, group_attn_kernel<true>}) {
+            e = cudaFuncSetAttribute(kf, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kGaSmemBytes));
+            if (e != cudaSuccess) return e;
+        }
+        for (const auto kf : {group_attn_few_kernel<false>, group_attn_few_kernel<true>}) {
+            e = cudaFuncSetAttribute(kf, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kGfSmemBytes));
+            if (e != cudaSuccess) return e;
+        }
         // One shared-memory carveout for every kernel of the path, so that
         // consecutive launches do not reconfigure the SMs' L1 / shared split.
         const void *kernels[] = {reinterpret_cast<const void *>(quant_kv_fp4_kernel),
@@ -100,8 +102,10 @@ cudaError_t device_info(DeviceInfo **out) {
                                  reinterpret_cast<const void *>(append_kv_rope_kernel),
                                  reinterpret_cast<const void *>(rope_rows_kernel<true>),
                                  reinterpret_cast<const void *>(rope_rows_kernel<false>),
-                                 reinterpret_cast<const void *>(group_attn_kernel),
-                                 reinterpret_cast<const void *>(group_attn_few_kernel),
+                                 reinterpret_cast<const void *>(group_attn_kernel<false>),
+                                 reinterpret_cast<const void *>(group_attn_kernel<true>),
+                                 reinterpret_cast<const void *>(group_attn_few_kernel<false>),
+                                 reinterpret_cast<const void *>(group_attn_few_kernel<true>),
                                  reinterpret_cast<const void *>(group_attn_merge_kernel)};
         for (const void *kf : kernels) {
             e = cudaFuncSetAttribute(kf, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
@@ -742,8 +746,11 @@ csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D, const csa2_
     const int64_t steps = tiles * (gap + std::max<int64_t>(1, (static_cast<int64_t>(max_pages) * kPage + blk - 1) / blk));
     const int ctas = static_cast<int>(std::min<int64_t>(std::min(dev->sm_count, kGaMaxCtas), steps));
     const int join = static_cast<int>(std::min<int64_t>(kGmCtasPerSm * dev->sm_count, kGmSlices * static_cast<int64_t>(N)));
-    const cudaError_t e = A.few ? launch_pdl(group_attn_few_kernel, dim3(ctas), dim3(kGaThreads), kGfSmemBytes, st, A)
-                                : launch_pdl(group_attn_kernel, dim3(ctas), dim3(kGaThreads), kGaSmemBytes, st, A);
+    // Outputs are moved out of tensor memory only where a range can have more blocks than go without it.
+    const bool moves = steps > static_cast<int64_t>(ctas) * (A.few ? kGfMove : kGaMove);
+    const auto kernel = A.few ? (moves ? group_attn_few_kernel<true> : group_attn_few_kernel<false>)
+                              : (moves ? group_attn_kernel<true> : group_attn_kernel<false>);
+    const cudaError_t e = launch_pdl(kernel, dim3(ctas), dim3(kGaThreads), A.few ? kGfSmemBytes : kGaSmemBytes, st, A);
     if (e != cudaSuccess) return CSA2_ERR_CUDA;
     return cuda_status(launch_pdl(group_attn_merge_kernel, dim3(join), dim3(kGmThreads), 0, st, A));
 }

@@ -39,7 +39,14 @@
 //               values. With the largest one at 2^0 a million entries 17.4
 //               below a sink were lost, 3% of the output. The sums are taken
 //               before, in fp32. Then they add the pieces, and at the end of a
-//               row tile write it.
+//               row tile write it. The tensor cores cut off what does not fit
+//               when they add to O (sums of one sign were short by 1.1e-3 after
+//               131,072 entries), so every kGaMove blocks O is moved out to the
+//               range's partial, added up there with rounding, and begins at
+//               zero again; after the last block the sum is brought back. The
+//               code for it costs 2 to 3% (64 tokens over 32,768 keys 106.7 us
+//               against 103.8), so calls whose ranges cannot be that long take
+//               a kernel without it (kMoves).
 //   warp 8      issues the MMAs, one lane under a predicate.
 //   warps 9-14  dequantise: E2M1 x E4M3 is exact in f16. The codes of the next
 //               block are in registers while this one is multiplied, and its
@@ -87,6 +94,7 @@ constexpr int kGaRegs = (kDim - kGaTmemCh) / 2;                    // outputs a 
 // A block's nine chunks are filled, multiplied and released in three rounds, in
 // the order in which O's MMAs are done with them: 2 r, 2 r + 1 and 6 + r.
 constexpr int kGaRounds = 3;
+constexpr int kGaMove = 512;                                       // blocks (32,768 entries) that O adds up by itself
 constexpr int kGaGap = 5;                                          // 2: 93 us for 8 groups of 64 tokens, 5: 74
 // log2 units: what a probability of the maximum is raised by, and a block may exceed that maximum by; f16 ends below 2^16.
 constexpr float kGaHead = 7.0f, kGaSlack = 8.0f;                   // 11 and 4: 4 tokens x 1M entries of wide scores 322 us against 274
@@ -269,6 +277,18 @@ __device__ __forceinline__ void ga_tmem_st16(uint32_t taddr, const uint32_t (&v)
           "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 32 lanes x 4 columns.
+__device__ __forceinline__ void ga_tmem_ld4(uint32_t taddr, float (&v)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void ga_tmem_st4(uint32_t taddr, const float (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n\t"
+                 "tcgen05.wait::st.sync.aligned;"
+                 ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
 }
 
 // 32 lanes x 32 columns.
@@ -511,6 +531,7 @@ __device__ __forceinline__ void ga_write16(const GaArgs &A, int64_t row, int ch,
     dst[1] = make_uint4(b[4], b[5], b[6], b[7]);
 }
 
+template <bool kMoves>
 __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk<GaWide> walk, int warp, int lane) {
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;      // keys 32 half ..; tile row
     const uint32_t tm = sm.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -533,9 +554,16 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk<G
         if (threadIdx.x == 0) mbar_arrive(&sm.q_full);
         const float scale = sm.scale[row];
         float m = -INFINITY, l = 0.0f;
+        [[maybe_unused]] float moved = 1.0f;                       // factor of what was moved out
         float2 acc[kGaRegs / 2];
 #pragma unroll
         for (int i = 0; i < kGaRegs / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+        // Part of a row tile, or what was moved out of one: unnormalised, 4 channels of a head together; only this
+        // thread's own. The slot is free for a tile that lies whole in the range: the first one's own, then the last's.
+        auto partial = [&]() {
+            const int64_t slot = 2 * blockIdx.x + (seg_no > 0);
+            return reinterpret_cast<float2 *>(A.part_o) + (slot * A.tok_slots + (row >> 4)) * (kDim * kHeads / 2) + 2 * (row & 15);
+        };
         // adds this half's columns of a piece
         auto piece_add = [&](auto n_, int to, uint64_t *full, uint64_t *empty, int col, uint32_t parity) {
             constexpr int kN = decltype(n_)::value;
@@ -596,6 +624,7 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk<G
                 const float f = raise ? ga_ex2(m - (mx - kGaHead)) : 1.0f;   // 0 for the first keys of a row
                 if (raise) m = mx - kGaHead;
                 l *= f;
+                if constexpr (kMoves) moved *= f;
 #pragma unroll
                 for (int i = 0; i < kGaRegs / 2; ++i) acc[i] = make_float2(acc[i].x * f, acc[i].y * f);
                 if (kb > s.k0) {                                   // O of the block before is complete
@@ -620,6 +649,32 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk<G
             piece_add(std::integral_constant<int, 16>{}, 32, &sm.dd_full, &sm.dd_empty, kGaDCol, 0u);
             piece_add(std::integral_constant<int, 32>{}, 48, &sm.ds_full, &sm.k_full[0], kGaSCol, 1u);
             piece_add(std::integral_constant<int, 16>{}, 80, &sm.dd_full, nullptr, kGaDCol, 1u);   // p_full says it next
+            if constexpr (!kMoves) continue;
+            const int done = kb + 1 - s.k0;
+            const bool last = kb + 1 == s.k1;
+            if (last ? done > kGaMove : done % kGaMove == 0) {
+                wait(&sm.k_free[kGaRounds - 1], par);              // O is complete
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < kGaTmemCh / 2; c += 4) {
+                    const int ch = half * (kGaTmemCh / 2) + c;
+                    float4 *const out = reinterpret_cast<float4 *>(partial() + ch / 4 * (2 * kHeads));
+                    const bool live = (row >> 4) < s.ntok;
+                    float a[4];
+                    ga_tmem_ld4(tm + ch, a);
+                    if (live && done > kGaMove) {
+                        const float4 v = *out;
+                        a[0] += moved * v.x;
+                        a[1] += moved * v.y;
+                        a[2] += moved * v.z;
+                        a[3] += moved * v.w;
+                    }
+                    if (live && !last) *out = make_float4(a[0], a[1], a[2], a[3]);
+                    if (!last) a[0] = a[1] = a[2] = a[3] = 0.0f;
+                    ga_tmem_st4(tm + ch, a);
+                }
+                moved = 1.0f;
+            }
         }
         // ---- end of the segment
         wait(&sm.k_free[kGaRounds - 1], (blk - 1) & 1u);
@@ -632,10 +687,9 @@ __device__ __forceinline__ void ga_softmax(const GaArgs &A, GaSmem &sm, GaWalk<G
         ga_pair_bar(pair_bar);
         l = sm.l[row];
         if (s.k0 > 0 || s.k1 < s.blocks) {
-            // part of a row tile: unnormalised, 4 channels of a head together. The sums in
-            // registers leave in pairs: as fours they would cost spilled registers.
+            // the sums in registers leave in pairs: as fours they would cost spilled registers
             const int64_t slot = 2 * blockIdx.x + (seg_no > 0);
-            float2 *po = reinterpret_cast<float2 *>(A.part_o) + (slot * A.tok_slots + tok) * (kDim * kHeads / 2) + 2 * h;
+            float2 *po = partial();
             if (live && half == 0) A.part_ml[(slot * A.tok_slots + tok) * kHeads + h] = make_float2(m, l);
 #pragma unroll 1
             for (int c = 0; c < kGaTmemCh / 2; c += 16) {
@@ -852,6 +906,7 @@ __device__ __forceinline__ void ga_mma(const GaArgs &A, GaSmem &sm, GaWalk<GaWid
     if (blk > 0) wait(&sm.k_free[kGaRounds - 1], (blk - 1) & 1u);
 }
 
+template <bool kMoves>
 __global__ void __launch_bounds__(kGaThreads, 1)
 group_attn_kernel(const GaArgs A) {
     extern __shared__ __align__(1024) uint8_t ga_raw[];
@@ -892,7 +947,7 @@ group_attn_kernel(const GaArgs A) {
     const GaWalk<GaWide> walk = sm.walk;
     if (warp < kGaSoftWarps) {
         ga_regs_up<kGaSoftRegs>();
-        ga_softmax(A, sm, walk, warp, lane);
+        ga_softmax<kMoves>(A, sm, walk, warp, lane);
     } else {
         ga_regs_down<kGaOtherRegs>();
         if (warp == kGaMmaWarp)

@@ -20,7 +20,8 @@
 //               when one of them exceeds its row's maximum so far by more than
 //               kGaSlack do all take the maxima over the keys (a transposing
 //               butterfly) and rescale.
-//               A row's sum is kept per key, 32 in registers, to the end.
+//               A row's sum is kept per key, 32 in registers, to the end. O is
+//               moved out every kGfMove blocks, as in K12 (its code costs 1%).
 //   warp 8      issues the MMAs, with 16 columns per token present.
 //   warps 9-15  dequantise, 16 keys each (112 = 7 x 16; 16 keys share a page).
 // The last 128 channels of O^T are 448 .. 575: 64 of them come twice. A tile's
@@ -51,6 +52,7 @@ constexpr int kGfTiles = 5;                                        // of 128 cha
 // Chunks of 64 channels are filled, multiplied and released in rounds: two for
 // each of O's first three tiles, three for the last two.
 constexpr int kGfRounds = 4;
+constexpr int kGfMove = 256;                                       // blocks (28,672 entries) that O adds up by itself
 constexpr float kGfNone = 1e30f;                                   // reference of a row without keys yet: any score exceeds it
 
 struct GfSmem {
@@ -63,6 +65,7 @@ struct GfSmem {
     alignas(16) float scale[kGfRows];                              // of a row: softmax scale (log2) times query exponent
     alignas(16) float nref[kGfRows];                               // minus its reference
     alignas(16) float fac[kGfRows], own[kGfRows];                  // factors of a rescaling, or of the entries and the own part
+    float moved[kGfRows];                                          // factor of what was moved out
     float m[kGfRows];                                              // its reference, -inf without keys yet
     float col[4][kGfRows];                                         // a row's maximum or sum in each quarter of the keys
     int64_t scan[kGaThreads / 32], start, total;
@@ -135,6 +138,7 @@ __device__ __forceinline__ bool gf_any(bool v) {
 // Channel of O^T's tile t in tensor memory lane `at`.
 __device__ __forceinline__ int gf_channel(int t, int at) { return (t < 4 ? 128 * t : 448) + at; }
 
+template <bool kMoves>
 __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<GaFew> walk, int warp, int lane) {
     const int quarter = warp & 3, half = warp >> 2, key = 32 * quarter + lane, tid = threadIdx.x;
     const uint32_t tm0 = sm.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -209,9 +213,11 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
                     float mx = fmaxf(fmaxf(sm.col[0][tid], sm.col[1][tid]), fmaxf(sm.col[2][tid], sm.col[3][tid]));
                     mx = mx == -INFINITY ? mx : mx * sm.scale[tid];
                     const float m = sm.m[tid];
-                        const bool raise = mx > m + (kGaHead + kGaSlack) || (m == -INFINITY && mx > m);
+                    const bool raise = mx > m + (kGaHead + kGaSlack) || (m == -INFINITY && mx > m);
                     mx -= kGaHead;
-                    sm.fac[tid] = raise ? ga_ex2(m - mx) : 1.0f;   // 0 for the first keys of a row
+                    const float f = raise ? ga_ex2(m - mx) : 1.0f; // 0 for the first keys of a row
+                    sm.fac[tid] = f;
+                    if constexpr (kMoves) sm.moved[tid] *= f;
                     if (raise) {
                         sm.m[tid] = mx;
                         sm.nref[tid] = -mx;
@@ -253,6 +259,33 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_full);
+            if constexpr (!kMoves) continue;
+            const int done = kb + 1 - s.k0;
+            const bool last = kb + 1 == s.k1;
+            if (last ? done > kGfMove : done % kGfMove == 0) {
+                wait(&sm.k_free[kGfRounds - 1], blk & 1u);         // O is complete
+                tc_fence_after();
+                const int64_t row0 = (2 * blockIdx.x + (seg_no > 0)) * static_cast<int64_t>(A.tok_slots) * kHeads + c0;
+#pragma unroll 1
+                for (int t = 0; t < kGfTiles; ++t)
+#pragma unroll 1
+                    for (int j = 0; j < 8 * live; j += 4) {
+                        if (t == kGfTiles - 1 && quarter < 2) break;       // channels 448-511 are in the tile before
+                        float a[4], *out = A.part_o + (row0 + j) * kDim + gf_channel(t, 32 * quarter + lane);
+                        const uint32_t at = tm + kGfOCol + t * kGfRows + j;
+                        ga_tmem_ld4(at, a);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (done > kGfMove) a[i] += sm.moved[c0 + j + i] * out[i * kDim];
+                            if (last) continue;
+                            out[i * kDim] = a[i];
+                            a[i] = 0.0f;
+                        }
+                        ga_tmem_st4(at, a);
+                    }
+                gf_bar();                                          // all have read their factors
+                if (tid < kGfRows) sm.moved[tid] = 1.0f;
+            }
         }
         // ---- end of the segment: the next one's queries first, so that its scores are computed meanwhile
         GaSeg n;
@@ -447,6 +480,7 @@ __device__ __forceinline__ void gf_mma(const GaArgs &A, GfSmem &sm, GaWalk<GaFew
     if (blk > 0) wait(&sm.k_free[kGfRounds - 1], (blk - 1) & 1u);
 }
 
+template <bool kMoves>
 __global__ void __launch_bounds__(kGaThreads, 1)
 group_attn_few_kernel(const GaArgs A) {
     extern __shared__ __align__(1024) uint8_t ga_raw[];
@@ -483,7 +517,7 @@ group_attn_few_kernel(const GaArgs A) {
     const GaWalk<GaFew> walk = sm.walk;
     if (warp < kGaSoftWarps) {
         ga_regs_up<kGaSoftRegs>();
-        gf_softmax(A, sm, walk, warp, lane);
+        gf_softmax<kMoves>(A, sm, walk, warp, lane);
     } else {
         ga_regs_down<kGaOtherRegs>();
         if (warp == kGaMmaWarp)

@@ -7,7 +7,9 @@ type); a score s is off by d (see test_gpu_group_attn.py), which moves every wei
 rounded to f16 after it was raised by 2^7: 2^-11 of itself, or where f16 has its fixed step 2^-24 by half of that,
 2^-32 of the largest weight, T of them together T 2^-32 max |v|. The products are added up in fp32 16 entries at a time;
 the tensor cores cut off what does not fit, at each of at most 4 additions 2^-23 of the sum so far, so n entries under one
-accumulator give n / 16 2^-21 A. Joining the ranges (at most 160) gives 160 2^-24 A. lse as in test_gpu_group_attn.py."""
+accumulator give n / 16 2^-21 A; n is 32,768 at most, then the sum is moved out and added up with rounding (T / 28672
+times at most, 2^-24 A each, the shorter of the two forms' distances). Joining the ranges (at most 160) gives
+160 2^-24 A. lse as in test_gpu_group_attn.py."""
 import math
 
 import pytest
@@ -17,7 +19,7 @@ from test_gpu_group_attn import DIM, H, PAGE, SCALE, lib      # noqa: F401 (lib 
 
 pytestmark = pytest.mark.gpu
 
-ONE, HALF_STEP = 0x38, 2.0 ** -32                        # E4M3's 1.0
+ONE, HALF_STEP, AT_ONCE = 0x38, 2.0 ** -32, 32768                       # E4M3's 1.0
 
 
 def sms():
@@ -49,7 +51,8 @@ def expect(v, count, s, own=None):
 
 
 def close(out, lse, o, A, L, d, T, at_once, top):
-    tol = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2 * d + at_once / 16 * 2.0 ** -21 + 160 * 2.0 ** -24) * A + T * HALF_STEP * top
+    sums = min(at_once, AT_ONCE) / 16 * 2.0 ** -21 + (T / 28672 + 160) * 2.0 ** -24
+    tol = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2 * d + sums) * A + T * HALF_STEP * top
     err = (out.double() - o).abs()
     assert bool((err <= tol).all()), f"off by {float((err / tol).max()):.2f} tolerances"
     tl = d[..., 0] + 2.0 ** -21 + (64 + T / 64) * 2.0 ** -24 + 2.0 ** -22 * L.abs()
@@ -93,6 +96,33 @@ def test_flat_tail_behind_a_dominant_entry(lib, few, at, own):
     out, lse = call(lib, cache, q.cuda(), table, T, groups, gpu)
     assert lib.last_device_error() == 0
     close(out, lse, *(t.cuda() for t in (o, A, L, d)), T, T, 1.0)
+
+
+@pytest.mark.parametrize("tiles,T", [(1, 1 << 20), (2.5, 131072), (2.5, 70000)])
+@pytest.mark.parametrize("few", [False, True])
+def test_sums_of_one_sign(lib, few, tiles, T):
+    """Equal values, joined with an own part that takes all of them away again, so that the result is the error of the
+    sum; two weights, so that no sum is exact. Row tiles that are a range each, and ranges of two and a half tiles."""
+    cache = lib.PagedCache(1)
+    cache.kv_scale.fill_(ONE)
+    cache.kv_fp4.fill_(0x22)                             # 1.0
+    cache.kv_fp4[0, ::2, 0] = 0x24                       # 2.0 in channel 0 of every other entry
+    n, tokens = int(tiles * sms()), 4 if few else 8
+    groups = n if few else 1
+    n *= tokens
+    q = torch.zeros(n, H, DIM, dtype=torch.bfloat16)
+    q[..., 0] = (1 + torch.arange(H) * 2.0).to(torch.bfloat16)
+    s = q[0, :, :1].double() * torch.tensor([2.0, 1.0]) * SCALE
+    count = torch.tensor([-(-T // 2), T // 2], dtype=torch.float64)
+    v = torch.ones(2, DIM, dtype=torch.float64)
+    v[0, 0] = 2.0
+    o, _, L = expect(v, count, s)
+    own = (-o.float().cuda()[None].expand(n, H, DIM).contiguous(), L.float().cuda()[None].expand(n, H).contiguous())
+    out, lse = call(lib, cache, q.cuda(), torch.zeros(-(-T // PAGE), dtype=torch.int32), T, groups, own)
+    assert lib.last_device_error() == 0
+    exact = expect(v, count, s, (own[0][0].double().cpu(), own[1][0].double().cpu()))
+    d = (576 * 2.0 ** -24 + 2.0 ** -21) * s[:, :1]
+    close(out, lse, *(t.cuda() for t in exact + (d,)), T, T, 2.0)
 
 
 @pytest.mark.parametrize("own", [False, True])
