@@ -125,12 +125,13 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8(const uint4 &v, float sdown) {
 // Power-of-two exponent e such that values up to m, scaled by 2^-e, are
 // represented in f16 without overflow and with full relative precision for
 // the largest ones: 0 for m in [2^-4, 2^15) (the common case, no scaling),
-// else the exponent that puts m near 2^10. Clamped to [-60, 60] (O is scaled
-// by 2^+-e in f32 around a window tile's products).
-__device__ __forceinline__ int f16_exponent(float m) {
+// else the exponent that puts m near 2^10. Clamped to [-limit, limit]: 60 where
+// O is scaled by 2^+-e in f32 around a window tile's products, at most 126 for
+// 2^+-e itself.
+__device__ __forceinline__ int f16_exponent(float m, int limit = 60) {
     if (!(m > 0.0f) || (m >= 0.0625f && m < 32768.0f)) return 0;
     const int e = static_cast<int>((__float_as_uint(m) >> 23) & 0xffu) - 127 - 10;
-    return max(-60, min(60, e));
+    return max(-limit, min(limit, e));
 }
 
 // Largest magnitude over the CTA (one CTA barrier; every thread gets it).

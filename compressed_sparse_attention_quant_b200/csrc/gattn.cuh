@@ -461,7 +461,7 @@ __device__ __forceinline__ void ga_load_q(const GaArgs &A, uint8_t *tile, float 
             mx = __uint_as_float(max(m2 & 0xffff0000u, m2 << 16));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const int eq = mx < INFINITY ? f16_exponent(mx) : 0;   // a row with inf or NaN stays one
+            const int eq = mx < INFINITY ? f16_exponent(mx, 120) : 0;   // any finite row fits; one with inf or NaN stays one
             // never 0: entries that do not count have a score of -inf, which has to stay one
             if (part == 0) scale[row] = fmaxf(fabsf(A.scale_log2) * exp2f(static_cast<float>(eq)), 1e-30f);
             if (!__any_sync(0xffffffffu, eq != 0)) break;

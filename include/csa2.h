@@ -498,12 +498,14 @@ csa2_status csa2_rope_rows(const void *x_bf16, int64_t x_stride, int64_t n_tok, 
  *   ws          device workspace of csa2_group_attn_workspace_bytes(N, G)
  *               bytes, 256-byte aligned, clobbered; calls that can overlap in
  *               time need workspaces of their own
- * Queries are carried in f16 under a power-of-two exponent per (token, head);
- * scores, maxima, sums and outputs are fp32. Probabilities are rounded to f16
- * for the product with the values only: each by 2^-11 of itself, or by 2^-32
- * of the row's largest one where that is more (below 2^-21 of it), so that a
- * flat tail of T entries behind a dominant one is off by at most T 2^-32 of
- * its values. lse has all of it. Limits: N <= 2^20, G <= 65535.
+ * Queries are carried in f16 under a power-of-two exponent per (token, head),
+ * whatever their (finite) magnitude; scores, maxima, sums and outputs are fp32.
+ * Scores scale * <q, key> must stay below 2^23 in magnitude, where fp32 ends to
+ * resolve differences of one. Probabilities are rounded to f16 for the product
+ * with the values only: each by 2^-11 of itself, or by 2^-32 of the row's
+ * largest one where that is more (below 2^-21 of it), so a flat tail of T
+ * entries behind a dominant one is off by at most T 2^-32 of its values. lse
+ * has all of it. Limits: N <= 2^20, G <= 65535.
  */
 size_t csa2_group_attn_workspace_bytes(int N, int G);
 csa2_status csa2_group_attn(const void *q_bf16, int N, int H, int D,

@@ -151,3 +151,32 @@ def test_a_million_entries(lib, tokens, groups, gain, own):
     out, lse = call(lib, cache, q, table, T, groups, part)
     assert lib.last_device_error() == 0
     close(out, lse, o, A, L, d, T, T * max(groups, -(-tokens // 8)) / sms() + 128, float(v.abs().max()))
+
+
+@pytest.mark.parametrize("power,scale", [(-130, SCALE), (20, SCALE), (24, -SCALE), (-100, 2.0 ** 98), (-62, 2.0 ** 60),
+                                         (70, 2.0 ** -69), (80, -2.0 ** -80), (113, 2.0 ** -113), (127, 2.0 ** -124)])
+@pytest.mark.parametrize("tokens,groups", [(9, 1), (4, 1)])
+def test_queries_of_any_finite_magnitude(lib, tokens, groups, power, scale):
+    """Queries of magnitude 2^power, from bf16's subnormal numbers to its largest, under scales that keep the scores below
+    2^23. Entries of two kinds, 1 and 0.5 in channel 0, the only one that the queries have."""
+    T, pages = 200, 4
+    g = torch.Generator().manual_seed(power + 200)
+    cache = lib.PagedCache(pages)
+    cache.kv_scale.fill_(ONE)
+    kv = torch.randint(0, 16, (pages, PAGE, DIM), generator=g, dtype=torch.uint8)
+    kv[..., 0] = 2                                       # 1.0, in every third entry 0.5
+    kv[:, ::3, 0] = 1
+    cache.kv_fp4.copy_((kv[..., 0::2] | kv[..., 1::2] << 4).cuda())
+    lut = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64)
+    v = lut[kv.view(-1, DIM)[:T].long()]
+    q = torch.zeros(tokens, H, DIM, dtype=torch.bfloat16)
+    q[..., 0] = 2.0 ** power * 1.25
+    s = q[0, :, :1].double() * v[:, 0] * scale
+    o, A, L = expect(v, torch.ones(T, dtype=torch.float64), s)
+    out, lse = call(lib, cache, q.cuda(), torch.arange(pages, dtype=torch.int32), T, groups, scale=scale)
+    assert lib.last_device_error() == 0
+    # the kinds' distance (64 at most where both weigh) is off by 2^-22 of itself for the scale and 2^-19 for the
+    # exponent's argument; lse by five roundings of its magnitude
+    tol = 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2.0 ** -15) * A + T * HALF_STEP * 6
+    assert bool(((out.cpu().double() - o).abs() <= tol).all())
+    assert bool(((lse.cpu().double() - L).abs() <= 2.0 ** -21 * s.abs().amax() + 2.0 ** -18).all())
