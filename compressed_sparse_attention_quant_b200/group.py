@@ -87,7 +87,7 @@ class LayerGroup:
         self._q_rot: Optional[torch.Tensor] = None         # rotated queries of the layer at hand
         self.joined: List[torch.Tensor] = []               # with a shared context: bf16 outputs and their lse
         self.joined_lse: List[torch.Tensor] = []
-        self._ws_grp: Dict[int, torch.Tensor] = {}
+        self._ws_grp: Optional[torch.Tensor] = None        # one for any number of groups: their calls follow one another
 
     def index(self, layer: int) -> torch.Tensor:
         """The top-k index tensor layer `layer` attends with (an alias for Reuse)."""
@@ -151,7 +151,7 @@ class LayerGroup:
                 lib.group_attn(ql.view(n, lib.HEADS, lib.DIM), cache, shared.page_table, shared.lens, shared.q_offsets,
                                self.scale, o_own=out[li].view(n, lib.HEADS, lib.DIM), lse_own=lse[li].view(n, lib.HEADS),
                                out=self.joined[li].view(n, lib.HEADS, lib.DIM),
-                               lse=self.joined_lse[li].view(n, lib.HEADS), ws=self._ws_grp[shared.lens.shape[0]])
+                               lse=self.joined_lse[li].view(n, lib.HEADS), ws=self._ws_grp)
 
     def _rotated(self, q: torch.Tensor, positions: torch.Tensor) -> torch.Tensor:
         if self._q_rot is None:
@@ -170,8 +170,9 @@ class LayerGroup:
                                                device=self.device))
                 self.joined_lse.append(torch.empty(self.B, self.Sq, lib.HEADS, dtype=torch.float32,
                                                    device=self.device))
-        if groups not in self._ws_grp:
-            self._ws_grp[groups] = lib.workspace(lib.group_attn_workspace_bytes(n, groups), self.device)
+        need = lib.group_attn_workspace_bytes(n, groups)   # the same for every number of groups
+        if self._ws_grp is None or self._ws_grp.numel() < need:
+            self._ws_grp = lib.workspace(need, self.device)
 
 
 class StepGraph:
