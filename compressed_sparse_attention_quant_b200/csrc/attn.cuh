@@ -12,14 +12,13 @@
 // are split into S runs, one CTA each (8 warps, two CTAs per SM), S chosen by
 // the host so that all CTAs fit one wave. A run writes the row's result when
 // S = 1; else an unnormalised partial (m, l, O) that K5 merges.
-//   set-up   before waiting for the selection of the previous kernel (the
-//            query is an input): the query row is rounded to f16 while its
-//            largest magnitude is taken, and written again under 2^-eq in the
-//            rare case that it asks for a power-of-two exponent eq != 0; it is
-//            stored in the QK operand order (qk_pos) and each warp takes its
-//            fragments with ldmatrix. The run's selected positions are then
-//            resolved to physical cache slots 12 tiles at a time (top-k index
-//            -> page table, all loads of a chunk in flight);
+//   set-up   the run's selected positions are resolved to physical cache slots
+//            12 tiles at a time (top-k index -> page table, all loads of a
+//            chunk in flight). While the first tile's records are fetched, the
+//            query row is rounded to f16 and its largest magnitude taken, and
+//            written again under 2^-eq in the rare case that it asks for a
+//            power-of-two exponent eq != 0; it is stored in the QK operand
+//            order (qk_pos) and each warp takes its fragments with ldmatrix;
 //   prefetch cp.async (16-byte and 4-byte LDGSTS, zero-filled for padding)
 //            fetches the next tile's packed FP4 records and scales as soon as
 //            the current tile's QK has consumed them, overlapping the softmax
@@ -256,48 +255,17 @@ sparse_attn_kernel(const AttParams P) {
     const int g = lane >> 2, tig = lane & 3;
     const int n_rows_swa = kWindow + P.Sq - 1;
 
-    // Inputs that no earlier kernel of the step writes are read before the
-    // wait for the selection: the query, the sequence length and (into L2)
-    // the sequence's page-table row. The query goes through the (still free)
-    // f16 tile: 16-byte loads, f16 rounding, a scatter into the QK operand
-    // order, then one ldmatrix per k-step. Warp (kg, cq) covers channels
-    // cq*144 .. +143.
-    const int kg = warp >> 2, cq = warp & 3;
-    uint32_t qa[9][4];
-    int eq = 0;
-    {
-        // f16 under 2^-eq: written with eq = 0 while the row's largest
-        // magnitude is taken, and written again in the (rare) case that it
-        // asks for another exponent
-        const uint4 *qg = reinterpret_cast<const uint4 *>(P.q + static_cast<int64_t>(row) * kHeads * kDim);
-        auto stage = [&](float sdown) -> float {
-            float mx = 0.0f;
-            for (int i = tid; i < kHeads * kDim / 8; i += kAttThreads) {
-                const int h = i / (kDim / 8), c = (i - h * (kDim / 8)) * 8;
-                const uint4 v = __ldg(qg + i);
-                mx = bf16x4_absmax(v, mx);
-                const uint4 f = bf16x8_to_f16x8(v, sdown);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int L = qk_pos(c + 2 * p);
-                    *reinterpret_cast<uint32_t *>(sm.kh + kh_off(h, L >> 3) + (L & 7) * 2) = (&f.x)[p];
-                }
-            }
-            return mx;
-        };
-        eq = f16_exponent(att_cta_max(sm, stage(1.0f)));
-        if (eq != 0) {
-            stage(exp2f(static_cast<float>(-eq)));
-            __syncthreads();
-        }
-#pragma unroll
-        for (int ks = 0; ks < 9; ++ks)
-            ldsm_x4(qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], sm.kh + kh_off(lane & 15, 18 * cq + 2 * ks + (lane >> 4)));
-    }
+    // Inputs that no kernel of this library writes are read before the wait for
+    // the selection: the sequence length and (into L2) the sequence's page-table
+    // row. The query may come from the kernel right in front (a rotation, a
+    // joined output): it is only brought to L2, where that kernel's writes
+    // reach the line, and read behind the wait.
+    const uint4 *qg = reinterpret_cast<const uint4 *>(P.q + static_cast<int64_t>(row) * kHeads * kDim);
+    if (tid < kHeads * kDim * 2 / 128) prefetch_l2_line(qg + tid * 8);
     int T = P.seq_lens[b];
     for (int i = tid * 32; i < P.max_pages; i += kAttThreads * 32)           // 128-byte lines of the row
         prefetch_l2_line(P.page_table + static_cast<int64_t>(b) * P.max_pages + i);
-    pdl_wait();                                         // the selection's indices are ready
+    pdl_wait();                                         // the selection's indices and the query are ready
     pdl_trigger();
 
     if (T < P.Sq || T > P.max_pages * kPage) {
@@ -372,6 +340,42 @@ sparse_attn_kernel(const AttParams P) {
     };
     if (n_it > 0) prefetch(tile0);
     cp_async_commit();
+
+    // The query goes through the (still free) f16 tile while the first records
+    // are on their way: 16-byte loads, f16 rounding, a scatter into the QK
+    // operand order, then one ldmatrix per k-step. Warp (kg, cq) covers
+    // channels cq*144 .. +143.
+    const int kg = warp >> 2, cq = warp & 3;
+    uint32_t qa[9][4];
+    int eq = 0;
+    {
+        // f16 under 2^-eq: written with eq = 0 while the row's largest
+        // magnitude is taken, and written again in the (rare) case that it
+        // asks for another exponent
+        auto stage = [&](float sdown) -> float {
+            float mx = 0.0f;
+            for (int i = tid; i < kHeads * kDim / 8; i += kAttThreads) {
+                const int h = i / (kDim / 8), c = (i - h * (kDim / 8)) * 8;
+                const uint4 v = qg[i];
+                mx = bf16x4_absmax(v, mx);
+                const uint4 f = bf16x8_to_f16x8(v, sdown);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int L = qk_pos(c + 2 * p);
+                    *reinterpret_cast<uint32_t *>(sm.kh + kh_off(h, L >> 3) + (L & 7) * 2) = (&f.x)[p];
+                }
+            }
+            return mx;
+        };
+        eq = f16_exponent(att_cta_max(sm, stage(1.0f)));
+        if (eq != 0) {
+            stage(exp2f(static_cast<float>(-eq)));
+            __syncthreads();
+        }
+#pragma unroll
+        for (int ks = 0; ks < 9; ++ks)
+            ldsm_x4(qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], sm.kh + kh_off(lane & 15, 18 * cq + 2 * ks + (lane >> 4)));
+    }
 
     for (int tile = tile0; tile < tile1; ++tile) {
         const int it = tile - tile0;

@@ -119,15 +119,14 @@ pool_topk_kernel(const PoolArgs A) {
     const int e0 = rank * A.slice;                              // this CTA's entries [e0, e1)
     const int e1 = min(e0 + A.slice, A.C);
 
-    // Inputs no earlier kernel of the step writes: the query and weights.
+    int T = A.given ? A.Sq : A.seq_lens[b];                     // no kernel of this library writes the lengths
+    pdl_wait();                                                 // the pool, the query and its weights may be the previous kernel's
+    pdl_trigger();
     if (!A.given) {
         if (tid < kIdxHeads * kIdxDim / 4)
-            fs.qb[tid] = __ldg(reinterpret_cast<const uint32_t *>(A.q_idx + static_cast<int64_t>(row) * kIdxHeads * kIdxDim) + tid);
+            fs.qb[tid] = reinterpret_cast<const uint32_t *>(A.q_idx + static_cast<int64_t>(row) * kIdxHeads * kIdxDim)[tid];
         if (tid < kIdxHeads) fs.w[tid] = A.w[static_cast<int64_t>(row) * kIdxHeads + tid];
     }
-    int T = A.given ? A.Sq : A.seq_lens[b];
-    pdl_wait();                                                 // the pool is written by the previous kernel
-    pdl_trigger();
     if (T < A.Sq || T > A.max_pages * kPage) {
         if (tid == 0 && rank == 0) flag_status(kStatusBounds);
         T = A.Sq - 1 - row % A.Sq;                              // no valid token for any query of the row

@@ -22,6 +22,10 @@
  *     library allocates nothing and never synchronises on the compute calls.
  *   - `stream` is a cudaStream_t passed as void*; NULL is the legacy default
  *     stream. Compute calls only enqueue work on it.
+ *   - Sequence lengths and page tables may be read while the kernel right in
+ *     front in the stream still runs, if that kernel lets its successor start
+ *     early (programmatic dependent launch): none that writes them may do so.
+ *     Everything else is read after the stream's earlier work.
  *   - Argument errors (null pointers, unsupported shapes, misaligned buffers,
  *     too small workspace) are detected on the host before anything is
  *     enqueued and returned as a status; nothing runs in that case.
