@@ -228,9 +228,8 @@ __device__ __forceinline__ void fp8_row_codes(const uint32_t (&w)[8], unsigned m
 __global__ void __launch_bounds__(kIdxQuantThreads, 3)
 quant_index_fp8_kernel(const uint4 *__restrict__ x, int64_t n_rows, uint2 *__restrict__ codes,
                        float *__restrict__ sigma) {
-    // No early start for the next kernel, and a fence at the end: the candidate
-    // pool's selection reads its query before it waits for its predecessor.
     pdl_wait();
+    pdl_trigger();
     const int part = threadIdx.x & (kIdxQuantTpr - 1);
     // Each thread keeps its next kIdxQuantStages rows in flight with cp.async
     // into its own shared-memory slots (no registers held, no barrier: a
@@ -271,7 +270,6 @@ quant_index_fp8_kernel(const uint4 *__restrict__ x, int64_t n_rows, uint2 *__res
             }
         }
     }
-    __threadfence();
 }
 
 // Grid: one wave of resident blocks (grid-stride loop), or fewer when the

@@ -273,13 +273,14 @@ inline cudaError_t launch_append_kv_rope(AppendArgs A, int sm_count, cudaStream_
 // copied, to another tensor only, before the angles. A token's heads are shared
 // out over CTAs while there are fewer CTAs than the GPU holds.
 //
-// Measured: 64 tokens of 16 x 576 channels 2.9 us from launch to launch, 16,384
-// tokens 134 us (93 by the bytes) and of 4 x 64 channels 9.8 us (2.6 by the
-// bytes: three waves of CTAs whose time is the latency of angles and fence, and
-// the conversions to and from binary64, four per pair).
+// Measured: 64 tokens of 16 x 576 channels 2.6 us from launch to launch, 16,384
+// tokens 134 us (93 by the bytes) and of 4 x 64 channels 8.6 us (2.6 by the
+// bytes: three waves of CTAs whose time is the latency of the angles, and the
+// conversions to and from binary64, four per pair). Without the early start of
+// the next kernel they took 2.9, 135 and 9.7.
 constexpr int kRrThreads = 256;
 constexpr int kRrTokens = 8;
-constexpr int kRrCtasPerSm = 6;                                   // 128K tokens of 4 x 64 channels: 5 72 us, 6 67, 8 63 but 64 tokens 3.3 against 2.9
+constexpr int kRrCtasPerSm = 6;                                   // without that start, 128K tokens of 4 x 64 channels: 5 72 us, 6 67, 8 63 but 64 tokens 3.3 against 2.9
 constexpr int kRrPairs = 320;                                     // angles held by a CTA (dim / 2 <= 288)
 
 struct RopeRowsArgs {
@@ -298,6 +299,7 @@ rope_rows_kernel(const RopeRowsArgs A) {
     __shared__ double2 s_cs[kRrPairs];                            // (cos, sin) of (token, pair)
     __shared__ bool s_ok[kRrTokens];
     pdl_wait();
+    pdl_trigger();
     const int tid = threadIdx.x, half = A.rope.half, lo = A.rope.offset, h0 = blockIdx.y * A.cta_heads;
     const int nh = min(A.cta_heads, A.heads - h0);
     const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * A.tokens;
@@ -391,7 +393,6 @@ rope_rows_kernel(const RopeRowsArgs A) {
             *reinterpret_cast<uint2 *>(out + to + half) = make_uint2(v.z, v.w);
         }
     }
-    __threadfence();
 }
 
 inline cudaError_t launch_rope_rows(RopeRowsArgs A, int sm_count, cudaStream_t stream) {
