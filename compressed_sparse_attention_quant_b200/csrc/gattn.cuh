@@ -17,9 +17,10 @@
 // (read by then) and two in columns of their own, and are added up in the
 // registers of the softmax threads, 96 each. Splitting the channels over two
 // CTAs would compute S twice. CTA pairs (cta_group::2) with each CTA
-// dequantising half of the block took 646 us where this form takes 318 (4
-// tokens over 1M keys): a hand-off between CTAs is about 1,000 cycles against
-// 330 inside one. Dequantising every block twice, so that S of the next could
+// dequantising half of the block took 111 us where single CTAs then took 124
+// (64 tokens over 32,768 keys), but 646 against 378 (4 tokens over 1M keys): a
+// hand-off between CTAs is about 1,000 cycles against 330 inside one. What they
+// taught made single CTAs 103 and 315. Dequantising every block twice, so that S of the next could
 // run during the softmax, took 7,400 cycles a block against 6,500 then.
 //
 // Q and K lie as slabs of 8 channels (16 bytes) per row: the K-major operand
@@ -62,11 +63,12 @@
 // is an mbarrier wait with a limit; a thread whose wait ran out goes on without
 // waiting, so that all reach the end.
 //
-// Bound and measured: about 4,950 cycles a block, of which S takes 2,150 (60
-// an MMA: its 6 KB of operands are 48 cycles of shared memory, and the block is
-// being written meanwhile), the softmax 1,100 in which the tensor pipe idles
-// (512 of them the exponentials), O 1,300 and the rest hand-offs. 64 tokens
-// over 32,768 keys: 103 us, 750 TFLOP/s, of it some 30 us for query tiles in, partials out and K13.
+// Bound and measured: 4,900 cycles a block (the slope over the length, at 1,965
+// MHz), of which S takes 2,150 (60 an MMA: its 6 KB of operands are 48 cycles of
+// shared memory, and the block is being written meanwhile), the softmax 1,100 in
+// which the tensor pipe idles (512 of them the exponentials), O 1,300 and the
+// rest hand-offs. 64 tokens over 32,768 keys: 103 us, 750 TFLOP/s: 69 for 27.7
+// blocks a CTA and 32 for query tiles in, partials out and K13.
 #pragma once
 
 #include "attn.cuh"

@@ -31,11 +31,17 @@
 // Bound and measured: shared-memory bandwidth. With 64 columns a block moves
 // 6 KB for each of 71 MMAs, 126 KB of entries and 14 KB of P, 4,400 cycles at
 // 128 B each, and the softmax, in which nothing moves because no chunk of K is
-// free before its MMAs, adds 1,400: some 6,400 cycles for 112 keys, against
-// 4,950 for 64 in K12; with 16 columns 5,600. 4 tokens over 1M keys 261 us
-// (K12 315), 64 groups of 1 token over 4,096 keys each 74 us (K12 99.5). At 5
-// or more tokens a group takes two tiles here, and K12 wins: 32 groups of 5
-// over 4,096 keys 88 us against 70, of 4 61 against 69.
+// free before its MMAs, adds 1,400. Measured (slope over the length, at 1,965
+// MHz) are 7,100 cycles for 112 keys when the entries come from L2 and 7,400
+// from DRAM: the other 1,300 are hand-offs between the roles. With two tokens
+// 6,500 and 6,900, with one 6,200 and 6,700; K12 takes 4,900 for 64 keys. 4
+// tokens over 1M keys 262 us (K12 315): 237 for 63.3 blocks a CTA, the rest as
+// in K12. 64 groups of 1 token over 4,096 keys each 74 us (K12 99.5). At 5 or
+// more tokens a group takes two tiles here, and K12 wins: 32 groups of 5 over
+// 4,096 keys 88 us against 70, of 4 61 against 69. The rule N <= 4 G takes the
+// mean, so a popular group among many small or empty ones comes here too: 64
+// tokens over 32,768 keys beside 20 groups of one over 4,096 take 167 us, and
+// 133 beside 19, which K12 gets.
 #pragma once
 
 #include "gattn.cuh"

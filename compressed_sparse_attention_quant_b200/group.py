@@ -17,9 +17,10 @@ owner's pool instead of the whole context.
 
 Three things a serving step needs beside the sparse attention are options of
 step(): latents and indexer keys that come unrotated from their projection
-(raw_append), queries that do (positions), and entries that many requests
-share, a common prompt for instance, which every token of a group attends to
-in full (shared).
+(raw_append), attention queries that do (positions), and entries that many
+requests share, a common prompt for instance, which every token of a group
+attends to in full (shared). Indexer queries come rotated and quantised
+(lib.rope_rows, lib.quant_indexer_fp8), their sigma multiplied into w.
 """
 from __future__ import annotations
 
@@ -37,7 +38,7 @@ class SharedContext:
     """Entries that groups of consecutive query tokens share: group g's are the first lens[g] of the pages
     page_table[g], and tokens[g] counts its query tokens (b * q_tokens + s, in order). Every token is in a group; one
     without shared entries is in a group of length 0. The tensors may be refreshed in place between replays, the
-    counts are fixed."""
+    counts are fixed. Groups without tokens only count towards the choice of the few-token form (csa2.h): leave them out."""
 
     def __init__(self, page_table: torch.Tensor, lens: torch.Tensor, tokens: Sequence[int]):
         if page_table.dim() != 2 or len(tokens) != page_table.shape[0] or tuple(lens.shape) != (len(tokens),):

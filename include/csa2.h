@@ -475,7 +475,10 @@ csa2_status csa2_rope_rows(const void *x_bf16, int64_t x_stride, int64_t n_tok, 
  * shares. Group g owns query tokens q_offsets[g] .. q_offsets[g + 1) and all of
  * them attend to the first kv_lens[g] entries of page_table[g] (keys = values,
  * no causal bound), read and dequantised once for up to 8 tokens x 16 heads (4
- * tokens when N <= 4 G, the form for few tokens per group):
+ * tokens when N <= 4 G, the form for few tokens per group; groups without
+ * tokens count, so leave them out where the other tokens are many in few
+ * groups: 200 tokens over 32,768 entries take 396 us beside 63 unused groups
+ * and 268 beside 40):
  *     out[n][h] = sum_t softmax_t(scale * <q, key_t>) * key_t
  *     lse[n][h] = log sum_t exp(scale * <q, key_t>)
  * With o_own and lse_own (a normalised result and its natural-log lse over
