@@ -153,6 +153,61 @@ def test_a_million_entries(lib, tokens, groups, gain, own):
     close(out, lse, o, A, L, d, T, T * max(groups, -(-tokens // 8)) / sms() + 128, float(v.abs().max()))
 
 
+@pytest.mark.parametrize("own", [False, True])
+@pytest.mark.parametrize("few", [False, True])
+def test_groups_about_the_distance_of_moving_out(lib, few, own):
+    """Groups whose row tiles are cut anywhere, of lengths about the distances at which outputs leave tensor memory, with
+    pages that are left out, entries whose scores grow half-way, and a workspace that holds anything."""
+    lens = [32768, 32769, 0, 28672, 28673, 65536, 65537, 57345, 200, 140001] * (10 if few else 1)
+    share = [3, 4, 2, 5, 1, 4, 0, 7, 4, 4] if few else [90, 64, 9, 130, 61, 40, 0, 77, 8, 210]
+    tokens = share * (10 if few else 1)
+    N, G, pages = sum(tokens), len(lens), 24
+    assert few == (N <= 4 * G)
+    g = torch.Generator().manual_seed(8)
+    cache = lib.PagedCache(pages)
+    n = pages * PAGE
+    x = torch.randn(n, DIM, generator=g) + 0.25
+    x[n // 2:, 0] += 6
+    lib.quant_kv_fp4(x.to(torch.bfloat16).cuda(), torch.arange(n, dtype=torch.int32).cuda(), cache)
+    lut = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64).cuda()
+    codes = torch.stack((cache.kv_fp4 & 15, cache.kv_fp4 >> 4), -1).flatten(-2).long()
+    v = (lut[codes].view(n, 36, 16) * cache.kv_scale.view(torch.float8_e4m3fn).double().view(n, 36, 1)).view(n, DIM)
+    W = max(-(-t // PAGE) for t in lens)
+    table = torch.randint(0, pages, (G, W), generator=g)
+    table[:, :W // 4] %= pages // 2
+    table[torch.rand(G, W, generator=g) < 0.02] = -1
+    q = torch.randn(N, H, DIM, generator=g)
+    q[:, ::2, 0] += 8
+    q = q.to(torch.bfloat16).cuda()
+    part = (None, None) if not own else (torch.randn(N, H, DIM, generator=g).cuda(), torch.randn(N, H, generator=g).cuda() + 11)
+    offs = [sum(tokens[:i]) for i in range(G + 1)]
+    got = []
+    for fill in (0, 0xFF):
+        ws = torch.full((lib.group_attn_workspace_bytes(N, G),), fill, dtype=torch.uint8, device="cuda")
+        got.append(lib.group_attn(q, cache, table.int().cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                                  torch.tensor(offs, dtype=torch.int32).cuda(), SCALE, *part, ws=ws))
+    assert lib.status_string(lib.last_device_error()) == "CSA2_ERR_DEVICE_BOUNDS"
+    (out, lse), again = got
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    for i, T in enumerate(lens):
+        a, b = offs[i], offs[i + 1]
+        if a == b:
+            continue
+        mine = None if not own else (part[0][a:b].double(), part[1][a:b].double())
+        t = torch.arange(T)
+        page = table[i][t // PAGE]
+        count = torch.bincount((page * PAGE + t % PAGE)[page >= 0], minlength=n).double().cuda()
+        if T == 0:
+            o = mine[0] if own else torch.zeros(b - a, H, DIM, dtype=torch.float64).cuda()
+            assert torch.equal(out[a:b], o.to(torch.bfloat16))
+            assert torch.equal(lse[a:b], part[1][a:b]) if own else bool((lse[a:b] == -math.inf).all())
+            continue
+        s = q[a:b].double() @ v.t() * SCALE
+        d = (576 * 2.0 ** -24 * SCALE * (q[a:b].double().abs() @ v.abs().t()) + 2.0 ** -21 * s.abs()).amax(-1, keepdim=True)
+        o, A, L = expect(v, count, s, mine)
+        close(out[a:b], lse[a:b], o, A, L, d, T, T, float(v.abs().max()))
+
+
 @pytest.mark.parametrize("power,scale", [(-130, SCALE), (20, SCALE), (24, -SCALE), (-100, 2.0 ** 98), (-62, 2.0 ** 60),
                                          (70, 2.0 ** -69), (80, -2.0 ** -80), (113, 2.0 ** -113), (127, 2.0 ** -124)])
 @pytest.mark.parametrize("tokens,groups", [(9, 1), (4, 1)])
