@@ -255,13 +255,26 @@ sparse_attn_kernel(const AttParams P) {
     const int g = lane >> 2, tig = lane & 3;
     const int n_rows_swa = kWindow + P.Sq - 1;
 
+    // tiles: ceil(k / 64) of selected entries (the last one padded), then the
+    // window's n_win tiles of 64 rows
+    const int n_fp4_tiles = (P.k + kAttTile - 1) / kAttTile;
+    const int n_tiles = n_fp4_tiles + P.n_win;
+    const int tile0 = split * P.tiles_per_split;
+    const int tile1 = min(tile0 + P.tiles_per_split, n_tiles);
+    const int n_it = max(tile1 - tile0, 0);
+
     // Inputs that no kernel of this library writes are read before the wait for
     // the selection: the sequence length and (into L2) the sequence's page-table
     // row. The query may come from the kernel right in front (a rotation, a
     // joined output): it is only brought to L2, where that kernel's writes
-    // reach the line, and read behind the wait.
+    // reach the line, and read behind the wait; so are the run's window rows,
+    // 9 lines each.
     const uint4 *qg = reinterpret_cast<const uint4 *>(P.q + static_cast<int64_t>(row) * kHeads * kDim);
     if (tid < kHeads * kDim * 2 / 128) prefetch_l2_line(qg + tid * 8);
+    const uint8_t *band = reinterpret_cast<const uint8_t *>(P.swa + (static_cast<int64_t>(b) * n_rows_swa + j) * kDim);
+    constexpr int kTileLines = kAttTile * kDim * 2 / 128;
+    for (int i = max(tile0 - n_fp4_tiles, 0) * kTileLines + tid; i < (tile1 - n_fp4_tiles) * kTileLines; i += kAttThreads)
+        prefetch_l2_line(band + i * 128);
     int T = P.seq_lens[b];
     for (int i = tid * 32; i < P.max_pages; i += kAttThreads * 32)           // 128-byte lines of the row
         prefetch_l2_line(P.page_table + static_cast<int64_t>(b) * P.max_pages + i);
@@ -272,14 +285,6 @@ sparse_attn_kernel(const AttParams P) {
         if (tid == 0 && split == 0) flag_status(kStatusBounds);
         T = -1;                                          // no valid key at all
     }
-    // tiles: ceil(k / 64) of selected entries (the last one padded), then the
-    // window's n_win tiles of 64 rows
-    const int n_fp4_tiles = (P.k + kAttTile - 1) / kAttTile;
-    const int n_tiles = n_fp4_tiles + P.n_win;
-    const int tile0 = split * P.tiles_per_split;
-    const int tile1 = min(tile0 + P.tiles_per_split, n_tiles);
-    const int n_it = max(tile1 - tile0, 0);
-
     if (tid < 16) {
         sm.m_run[tid] = -INFINITY;
         sm.l_run[tid] = 0.0f;
