@@ -20,8 +20,9 @@
 // dequantising half of the block took 111 us where single CTAs then took 124
 // (64 tokens over 32,768 keys), but 646 against 378 (4 tokens over 1M keys): a
 // hand-off between CTAs is about 1,000 cycles against 330 inside one. What they
-// taught made single CTAs 103 and 315. Dequantising every block twice, so that S of the next could
-// run during the softmax, took 7,400 cycles a block against 6,500 then.
+// taught made single CTAs 103 and 315. Dequantising every block twice, so that
+// S of the next could run during the softmax, took 7,400 cycles a block against
+// 6,500 then.
 //
 // Q and K lie as slabs of 8 channels (16 bytes) per row: the K-major operand
 // layout of S and the MN-major one of O, so a block is dequantised once for

@@ -164,6 +164,7 @@ __device__ __forceinline__ void gf_softmax(const GaArgs &A, GfSmem &sm, GaWalk<G
     auto reset = [&]() {
         sm.m[tid] = -INFINITY;
         sm.nref[tid] = kGfNone;
+        if constexpr (kMoves) sm.moved[tid] = 1.0f;
     };
     GaSeg s;
     uint32_t seg_no = 0;

@@ -503,8 +503,8 @@ csa2_status csa2_rope_rows(const void *x_bf16, int64_t x_stride, int64_t n_tok, 
  *               may overlap another argument (CSA2_ERR_INVALID_ARG where it
  *               meets the query, the own part or the workspace).
  *   ws          device workspace of csa2_group_attn_workspace_bytes(N, G)
- *               bytes (the same for every G), 256-byte aligned, clobbered; calls that can overlap in
- *               time need workspaces of their own
+ *               bytes (the same for every G), 256-byte aligned, clobbered;
+ *               calls that can overlap in time need workspaces of their own
  * Queries are carried in f16 under a power-of-two exponent per (token, head),
  * whatever their (finite) magnitude; scores, maxima, sums and outputs are fp32.
  * Scores scale * <q, key> must stay below 2^23 in magnitude, where fp32 ends to
